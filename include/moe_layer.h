@@ -93,6 +93,56 @@ typedef struct moe_layer *moe_handle;
  * synchronisation.  On success *out is a new handle (free it with moe_layer_destroy). */
 moe_status moe_layer_init(const moe_config *cfg, const moe_weights *w, moe_handle *out);
 
+/* ------------------------------------------------------------------------ MXFP4 experts
+ * Microscaled 4-bit floating point (MXFP4): a matrix [rows, cols], cols a multiple of 32, held as
+ *   codes  [rows, cols / 2] bytes   two e2m1 values a byte, the lower column in the low nibble:
+ *                                   bit 3 the sign, 0..7 the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   scales [rows, cols / 32] bytes  one e8m0 exponent for 32 neighbours of a row: 2^(byte - 127);
+ *                                   byte 255 is NaN
+ * value = e2m1 * 2^(byte - 127).
+ *
+ * moe_mxfp4_quantize: src [rows, cols] (fp32 or bf16, row-major, 16-byte aligned) -> codes (16-byte
+ * aligned) and scales.  For each block of 32: s = floor(log2 max|v|) - 2, at least -127; byte =
+ * s + 127; each code is the e2m1 value nearest to v / 2^s, ties to the even code, magnitudes past
+ * 6 saturating to 6 (a value keeps its sign when it rounds to zero).  A block of zeros gets byte 0.
+ * A block that holds an infinity or a NaN becomes NaN (byte 255, codes 0).
+ * moe_mxfp4_dequantize: the values, fp32 or bf16 (dst 16-byte aligned).  Exact in both types for
+ * bytes up to 252, the largest that moe_mxfp4_quantize writes; above, a code whose value is past
+ * the type's range becomes infinite.
+ * Both are asynchronous on `stream` and need no handle; rows or cols of 0 do nothing;
+ * MOE_ERR_INVALID_ARG for a null pointer, negative size, cols not a multiple of 32 or unknown
+ * dtype. */
+moe_status moe_mxfp4_quantize(const void *src, moe_dtype dtype, long long rows, int cols,
+                              uint8_t *codes, uint8_t *scales, void *stream);
+moe_status moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, long long rows,
+                                int cols, void *dst, moe_dtype dtype, void *stream);
+
+/* Caller-owned device pointers of a layer whose expert weights are MXFP4: the router as in
+ * moe_weights (bf16), the codes of w_gate, w_up [G, f, d / 2] and w_down [G, d, f / 2], and their
+ * scales [G, f, d / 32] and [G, d, f / 32], every pointer 16-byte aligned. */
+typedef struct {
+  const void *w_router;
+  const float *router_bias; /* may be null: zero bias */
+  const uint8_t *w_gate;
+  const uint8_t *w_up;
+  const uint8_t *w_down;
+  const uint8_t *scale_gate;
+  const uint8_t *scale_up;
+  const uint8_t *scale_down;
+} moe_mxfp4_weights;
+
+/* moe_layer_init over MXFP4 expert weights (cfg->dtype must be MOE_BF16, the type of the router
+ * and the activations).  On such a handle moe_forward and moe_forward_few compute the layer above
+ * with the weights' values as they stand (no rounding of x to fewer bits); the routing calls,
+ * moe_router_stats, moe_update_router_bias, the workspace and status calls and moe_set_option work as
+ * on any handle (the launch-plan options change nothing).  Training, per-stage events and
+ * expert health read bf16 weights: moe_backward*, moe_forward_save, moe_forward_profiled and
+ * moe_expert_health return MOE_ERR_UNSUPPORTED, and so does moe_forward_partial.  Products are
+ * accumulated in fp32; weights whose scale byte is 0 (2^-127) count as they stand only down to
+ * fp32's smallest normal number. */
+moe_status moe_layer_init_mxfp4(const moe_config *cfg, const moe_mxfp4_weights *w,
+                                moe_handle *out);
+
 /* Releases the host-side handle.  Does not touch any device buffer. */
 moe_status moe_layer_destroy(moe_handle h);
 
@@ -165,6 +215,21 @@ moe_status moe_route_from_logits(moe_handle h, const float *logits, int n_tokens
  * combine sums them in a fixed order in fp32 before one rounding to the output type. */
 moe_status moe_forward(moe_handle h, const void *x, int n_tokens, void *out, void *ws,
                        size_t ws_bytes, void *stream);
+
+/* The whole layer for a few tokens in ONE launch (bf16 and MXFP4 handles): router, selection,
+ * experts and combine in a persistent kernel that streams the chosen experts' weights without a
+ * pause between the projections.  The same mathematics as moe_forward, and its selection bit for
+ * bit; sums run in another fixed order (deterministic).  bf16 weights: h is rounded to bf16 as in
+ * moe_forward; MXFP4: to 11 bits.  moe_forward of an MXFP4 handle is this call where it is
+ * supported.
+ * At most 64 tokens, n_tokens * top_k <= 512, n_experts <= 288, d_model <= 8192; otherwise, and
+ * for fp32 layers and expert-parallel slices, MOE_ERR_UNSUPPORTED.  A cooperative launch with one
+ * block on each SM: it starts when the whole device is free of blocks that hold their SMs'
+ * shared memory, may be captured into a CUDA graph, and returns MOE_ERR_CUDA on a device
+ * partition that cannot hold the grid.  Leaves no h for moe_expert_health.  ws as for
+ * moe_forward; calls that share a workspace must not overlap. */
+moe_status moe_forward_few(moe_handle h, const void *x, int n_tokens, void *out, void *ws,
+                           size_t ws_bytes, void *stream);
 
 /* moe_forward that also records caller-created CUDA events (cudaEvent_t, passed as void*)
  * on `stream` around its kernel stages, for per-kernel timing with no profiler attached:

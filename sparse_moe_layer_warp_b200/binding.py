@@ -34,7 +34,9 @@ EXPORTS = ("moe_layer_init", "moe_layer_destroy", "moe_workspace_size", "moe_wor
            "moe_backward_workspace_size", "moe_saved_size", "moe_forward_save",
            "moe_backward_saved", "moe_backward_ex", "moe_set_option", "moe_layer_init_ep",
            "moe_forward_partial", "moe_ep_plan", "moe_ep_pack", "moe_ep_combine",
-           "moe_gemm_clock")
+           "moe_gemm_clock", "moe_mxfp4_quantize", "moe_mxfp4_dequantize",
+           "moe_layer_init_mxfp4", "moe_forward_few")
+MXFP4_BLOCK = 32  # values that share a scale
 MOE_BACKWARD_OVERWRITE = 1
 MOE_OPTION_H_HANDOVER = 1
 MOE_OPTION_SHARED_SIDE_SMS = 2
@@ -56,6 +58,12 @@ class moe_weights(ctypes.Structure):
     _fields_ = [("w_router", ctypes.c_void_p), ("router_bias", ctypes.c_void_p),
                 ("w_gate", ctypes.c_void_p), ("w_up", ctypes.c_void_p),
                 ("w_down", ctypes.c_void_p)]
+
+
+class moe_mxfp4_weights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w_router", "router_bias", "w_gate", "w_up",
+                                               "w_down", "scale_gate", "scale_up",
+                                               "scale_down")]
 
 
 class MoEError(RuntimeError):
@@ -108,6 +116,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.moe_ep_plan.argtypes = [P, P, I, I, P, P, P, P, P, Z, P]
         lib.moe_ep_pack.argtypes = [P, P, P, P, I, I, P, P, P, P, P, P]
         lib.moe_ep_combine.argtypes = [P, P, P, P, P, I, I, P, P]
+        lib.moe_mxfp4_quantize.argtypes = [P, I, ctypes.c_longlong, I, P, P, P]
+        lib.moe_mxfp4_dequantize.argtypes = [P, P, ctypes.c_longlong, I, P, I, P]
+        lib.moe_layer_init_mxfp4.argtypes = [ctypes.POINTER(moe_config),
+                                             ctypes.POINTER(moe_mxfp4_weights),
+                                             ctypes.POINTER(P)]
+        lib.moe_forward_few.argtypes = [P, P, I, P, P, Z, P]
         lib.moe_forward_launch_count.argtypes = [P, I]
         lib.moe_forward_launch_count.restype = I
         lib.moe_status_string.argtypes = [I]
@@ -119,7 +133,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                      "moe_expert_health", "moe_backward", "moe_forward_save",
                      "moe_backward_saved", "moe_backward_ex", "moe_set_option", "moe_layer_init_ep",
                      "moe_forward_partial", "moe_ep_plan", "moe_ep_pack", "moe_ep_combine",
-                     "moe_gemm_clock"):
+                     "moe_gemm_clock", "moe_mxfp4_quantize", "moe_mxfp4_dequantize",
+                     "moe_layer_init_mxfp4", "moe_forward_few"):
             getattr(lib, name).restype = I
         _lib = lib
     return _lib
@@ -177,6 +192,18 @@ def moe_layer_init_ep(cfg: moe_config, expert_begin: int, expert_end: int, w_rou
     _check("moe_layer_init_ep", lib.moe_layer_init_ep(ctypes.byref(cfg), ctypes.byref(w),
                                                       int(expert_begin), int(expert_end),
                                                       ctypes.byref(h)))
+    return h
+
+
+def moe_layer_init_mxfp4(cfg: moe_config, w_router, router_bias, w_gate, w_up, w_down):
+    """Handle of a layer over MXFP4 expert weights: w_gate, w_up, w_down are (codes, scales)."""
+    lib = load_library()
+    w = moe_mxfp4_weights(_addr(w_router), None if router_bias is None else _addr(router_bias),
+                          *(_addr(t[0]) for t in (w_gate, w_up, w_down)),
+                          *(_addr(t[1]) for t in (w_gate, w_up, w_down)))
+    h = ctypes.c_void_p()
+    _check("moe_layer_init_mxfp4", lib.moe_layer_init_mxfp4(ctypes.byref(cfg), ctypes.byref(w),
+                                                            ctypes.byref(h)))
     return h
 
 
@@ -248,6 +275,32 @@ def moe_forward(handle, x, n_tokens, out, ws, stream=None) -> None:
     _check("moe_forward", load_library().moe_forward(
         handle, _p(x), int(n_tokens), _p(out), _p(ws), ws.numel() * ws.element_size(),
         _stream(stream)))
+
+
+def moe_forward_few(handle, x, n_tokens, out, ws, stream=None) -> None:
+    """The whole layer for a few tokens in one launch (see include/moe_layer.h)."""
+    _check("moe_forward_few", load_library().moe_forward_few(
+        handle, _p(x), int(n_tokens), _p(out), _p(ws), ws.numel() * ws.element_size(),
+        _stream(stream)))
+
+
+_DTYPE_CODE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def moe_mxfp4_quantize(src, codes, scales, stream=None) -> None:
+    """codes and scales of `src` [.., cols] (fp32 or bf16; see include/moe_layer.h)."""
+    cols = int(src.shape[-1])
+    _check("moe_mxfp4_quantize", load_library().moe_mxfp4_quantize(
+        _p(src), _DTYPE_CODE[src.dtype], src.numel() // max(cols, 1), cols, _p(codes),
+        _p(scales), _stream(stream)))
+
+
+def moe_mxfp4_dequantize(codes, scales, dst, stream=None) -> None:
+    """The values that codes and scales stand for, into `dst` [.., cols] (fp32 or bf16)."""
+    cols = int(dst.shape[-1])
+    _check("moe_mxfp4_dequantize", load_library().moe_mxfp4_dequantize(
+        _p(codes), _p(scales), dst.numel() // max(cols, 1), cols, _p(dst),
+        _DTYPE_CODE[dst.dtype], _stream(stream)))
 
 
 def moe_backward_workspace_size(handle, n_tokens: int) -> int:
@@ -366,6 +419,45 @@ def moe_gemm_clock(handle, ws, stream=None) -> tuple:
     return float(mhz[0]), float(mhz[1])
 
 
+# ------------------------------------------------------------------ MXFP4 matrices
+def mxfp4_quantize(w, stream=None):
+    """(codes [.., cols / 2], scales [.., cols / 32]), uint8, of `w` [.., cols] (fp32 or bf16,
+    contiguous, cols a multiple of 32): MXFP4, one power-of-two scale for 32 neighbours."""
+    if w.dtype not in _DTYPE_CODE:
+        raise ValueError(f"w: expected fp32 or bf16, got {w.dtype}")
+    if w.dim() < 1 or w.shape[-1] % MXFP4_BLOCK:
+        raise ValueError(f"w: the last dimension must be a multiple of {MXFP4_BLOCK}, got shape "
+                         f"{tuple(w.shape)}")
+    _addr(w)
+    lead, cols = tuple(w.shape[:-1]), int(w.shape[-1])
+    codes = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=w.device)
+    scales = torch.empty(lead + (cols // MXFP4_BLOCK,), dtype=torch.uint8, device=w.device)
+    if w.numel():
+        with torch.cuda.device(w.device):
+            moe_mxfp4_quantize(w, codes, scales, stream)
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
+    """The values [.., cols] that codes [.., cols / 2] and scales [.., cols / 32] stand for."""
+    if dtype not in _DTYPE_CODE:
+        raise ValueError(f"dtype: expected fp32 or bf16, got {dtype}")
+    if codes.dim() < 1 or (2 * codes.shape[-1]) % MXFP4_BLOCK:
+        raise ValueError(f"codes: the last dimension must be a multiple of {MXFP4_BLOCK // 2}, "
+                         f"got shape {tuple(codes.shape)}")
+    lead, cols = tuple(codes.shape[:-1]), 2 * int(codes.shape[-1])
+    _expect(codes, lead + (cols // 2,), torch.uint8, "codes")
+    _expect(scales, lead + (cols // MXFP4_BLOCK,), torch.uint8, "scales")
+    _addr(codes)
+    if scales.device != codes.device:
+        raise ValueError(f"scales: on {scales.device}, codes on {codes.device}")
+    out = torch.empty(lead + (cols,), dtype=dtype, device=codes.device)
+    if out.numel():
+        with torch.cuda.device(codes.device):
+            moe_mxfp4_dequantize(codes, scales, out, stream)
+    return out
+
+
 # ------------------------------------------------------------------ convenience wrapper
 def _expect(t, shape, dtype, name):
     """The C ABI sees only pointers: a tensor of another shape or type would be read or
@@ -434,6 +526,25 @@ class MoELayer:
         _expect(out, x.shape, x.dtype, "out")
         moe_forward(self.handle, x, T, out, self.workspace(T), stream)
         return out
+
+    def forward_few(self, x, out=None, stream=None):
+        """forward for a few tokens in one launch (bf16; limits in include/moe_layer.h)."""
+        T = self._rows(x)
+        out = torch.empty_like(x) if out is None else out
+        _expect(out, x.shape, x.dtype, "out")
+        moe_forward_few(self.handle, x, T, out, self.workspace(T), stream)
+        return out
+
+    def to_mxfp4(self, max_tokens: int | None = None) -> "MoELayerMXFP4":
+        """A serving layer with this bf16 layer's router and its expert weights in MXFP4."""
+        if self.dtype != torch.bfloat16:
+            raise ValueError("to_mxfp4: a bf16 layer is needed")
+        w_router, bias, w_gate, w_up, w_down = self.tensors
+        return MoELayerMXFP4(w_router, bias, mxfp4_quantize(w_gate), mxfp4_quantize(w_up),
+                             mxfp4_quantize(w_down), top_k=self.k,
+                             max_tokens=max_tokens or int(self.cfg.max_tokens),
+                             n_shared=int(self.cfg.n_shared),
+                             routed_scale=float(self.cfg.routed_scale))
 
     def route(self, x=None, logits=None, want_logits=False, stream=None):
         if x is not None:
@@ -565,3 +676,40 @@ class MoELayer:
             self.close()
         except Exception:
             pass
+
+
+class MoELayerMXFP4(MoELayer):
+    """MoELayer over MXFP4 expert weights, for serving: w_gate, w_up [E + n_shared, f, d] and
+    w_down [E + n_shared, d, f] are (codes, scales) as mxfp4_quantize returns them; the router and
+    the activations are bf16.  forward, forward_few, route and router_stats as in MoELayer;
+    training calls and expert_health are refused by the library (MoEError)."""
+
+    def __init__(self, w_router, router_bias, w_gate, w_up, w_down, top_k: int,
+                 max_tokens: int, n_shared: int = 1, routed_scale: float = 1.0):
+        if w_router.dtype != torch.bfloat16 or w_router.dim() != 2:
+            raise ValueError("w_router: expected a [E, d] bf16 tensor")
+        E, d = w_router.shape
+        G = int(E) + int(n_shared)
+        if len(w_gate) != 2 or w_gate[0].dim() != 3:
+            raise ValueError("w_gate: expected (codes [G, f, d / 2], scales [G, f, d / 32])")
+        f = int(w_gate[0].shape[1])
+        for name, w, rows, cols in (("w_gate", w_gate, f, d), ("w_up", w_up, f, d),
+                                    ("w_down", w_down, d, f)):
+            codes, scales = w
+            _expect(codes, (G, rows, cols // 2), torch.uint8, f"{name} codes")
+            _expect(scales, (G, rows, cols // MXFP4_BLOCK), torch.uint8, f"{name} scales")
+        if router_bias is not None:
+            _expect(router_bias, (E,), torch.float32, "router_bias")
+        self.cfg = moe_config(int(max_tokens), int(d), int(E), int(top_k), int(f),
+                              int(n_shared), MOE_BF16, float(routed_scale))
+        self.handle = None
+        self.tensors = (w_router, router_bias, tuple(w_gate), tuple(w_up), tuple(w_down))
+        self.handle = moe_layer_init_mxfp4(self.cfg, *self.tensors)
+        self.device = w_router.device
+        self.dtype = w_router.dtype
+        self.ws = None
+        self.bw_ws = None
+        self.E, self.k, self.d = int(E), int(top_k), int(d)
+
+    def to_mxfp4(self, max_tokens: int | None = None):
+        raise ValueError("to_mxfp4: the layer holds MXFP4 weights already")

@@ -32,9 +32,11 @@
 #include "grouped_gemm.cuh"
 #include "grouped_gemm_bw.cuh"
 #include "grouped_gemm_pair.cuh"
+#include "mxfp4.cuh"
 #include "ptx_sm100.cuh"
 #include "router_stats.cuh"
 #include "routing.cuh"
+#include "weight_stream.cuh"
 
 using namespace moe;
 
@@ -70,6 +72,11 @@ struct moe_layer {
   int side_sms;
   cudaStream_t side;
   cudaEvent_t ev_fork, ev_join;
+  // MXFP4 expert weights (moe_layer_init_mxfp4): w holds the codes, these the scales
+  int mx;
+  const uint8_t *sc_gate, *sc_up, *sc_down;
+  // the expert weights as the weight-streaming kernel loads them (bf16 or code bytes)
+  CUtensorMap tm_st_g, tm_st_u, tm_st_d;
 };
 
 namespace {
@@ -119,6 +126,22 @@ bool encode_f32_2d(CUtensorMap *m, void *base, uint64_t cols, uint64_t rows) {
   cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// Row-major bytes [rows, cols] -> tiled map with box {128 bytes, box_rows rows} and 128-byte
+// swizzle (MXFP4 codes: 256 columns of K a box row).
+bool encode_u8_2d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows,
+                  uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
@@ -176,7 +199,7 @@ size_t esize(const moe_config &c) { return c.dtype == MOE_BF16 ? 2 : 4; }
 // Workspace regions (256-byte aligned).  P = T*k + n_shared*T rows of the sorted space.
 struct WsLayout {
   size_t status, logits, part, idx, gate, counts, offsets, perm, slot_row, chunk_hist, stats,
-      xs, h, y, done, health, total;
+      xs, h, y, done, health, xq, hq, total;
 };
 
 int pick_bn(const moe_config &c, int T, int mode);
@@ -187,7 +210,8 @@ bool up_gathers_rows(const moe_config &c, int T) {
   return pick_bn(c, T, MODE_UP) <= kGatherMaxBN;
 }
 
-WsLayout ws_layout(const moe_config &c, int T) {
+// mx: an MXFP4 handle's layout (block-scaled fp16 x and h of the weight-streaming kernel)
+WsLayout ws_layout(const moe_config &c, int T, bool mx = false) {
   WsLayout L;
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -214,9 +238,12 @@ WsLayout ws_layout(const moe_config &c, int T) {
   L.xs = (c.dtype == MOE_BF16 && !up_gathers_rows(c, T)) ? take(Tk * c.d_model * 2) : off;
   L.h = take(P * c.d_ff * esize(c));
   L.y = take(P * c.d_model * 4);  // fp32 in both precisions
-  L.done = take(((size_t)c.n_experts + c.n_shared) * 4);  // per-group up completion counts
+  // per-group up completion counts, then the weight-streaming kernel's per-tile y counts
+  L.done = take(((size_t)c.n_experts + c.n_shared + c.d_model / kStreamMinTile) * 4);
   // expert health: slice sums of squares, activations then parameters
   L.health = take(2 * ((size_t)c.n_experts + c.n_shared) * kHealthSlices * 8);
+  L.xq = take(mx ? (size_t)T * act_chunks(c.d_model) * kActChunkBytes : 0);
+  L.hq = take(mx ? P * act_chunks(c.d_ff) * kActChunkBytes : 0);
   L.total = off;
   return L;
 }
@@ -653,7 +680,7 @@ __global__ void __launch_bounds__(32) wait_timeout_selftest_kernel(DevStatus *st
   abort_flag = 0;
   mbar_wait_bounded(&bar, 0, &abort_flag, status, 101, limit_ns);
   abort_flag = 0;
-  int *flag = &status->pad[25];
+  int *flag = &status->pad[9];
   *flag = 0;
   counter_wait_bounded(flag, 1, &abort_flag, status, 102, limit_ns);
 }
@@ -664,7 +691,7 @@ moe_status check_call(const moe_layer *L, int T, void *ws, size_t ws_bytes) {
   if (!L) return MOE_ERR_INVALID_ARG;
   if (T < 0 || T > L->cfg.max_tokens) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
-  if (!ws || ws_bytes < ws_layout(L->cfg, T).total) return MOE_ERR_WORKSPACE;
+  if (!ws || ws_bytes < ws_layout(L->cfg, T, L->mx != 0).total) return MOE_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return MOE_ERR_ALIGNMENT;
   return MOE_OK;
 }
@@ -688,7 +715,7 @@ const char *moe_status_string(moe_status s) {
 }
 
 static moe_status layer_init(const moe_config *cfg, const moe_weights *w, int e0, int e1,
-                             moe_handle *out) {
+                             moe_handle *out, const moe_mxfp4_weights *mx = nullptr) {
   if (!cfg || !w || !out) return MOE_ERR_INVALID_ARG;
   *out = nullptr;
   const moe_config c = *cfg;
@@ -743,7 +770,28 @@ static moe_status layer_init(const moe_config *cfg, const moe_weights *w, int e0
     L->handover_fits = up_grids_fit(L);
     cudaGetLastError();  // an unavailable cluster query only disables the pair path
     const uint64_t G = (uint64_t)(e1 - e0) + c.n_shared;  // weight groups held
-    if (!encode_bf16_2d(&L->tm_wg, w->w_gate, c.d_model, G * c.d_ff, kBM) ||
+    if (mx) {
+      L->mx = 1;
+      L->sc_gate = mx->scale_gate;
+      L->sc_up = mx->scale_up;
+      L->sc_down = mx->scale_down;
+      if (!encode_u8_2d(&L->tm_st_g, w->w_gate, c.d_model / 2, G * c.d_ff, 32) ||
+          !encode_u8_2d(&L->tm_st_u, w->w_up, c.d_model / 2, G * c.d_ff, 32) ||
+          !encode_u8_2d(&L->tm_st_d, w->w_down, c.d_ff / 2, G * c.d_model, 32) ||
+          !encode_bf16_2d(&L->tm_wr, w->w_router, c.d_model, c.n_experts, kBM) ||
+          (router_half_tile(c) &&
+           !encode_bf16_2d(&L->tm_wr2, w->w_router, c.d_model, c.n_experts,
+                           (uint32_t)router_half_tile(c)))) {
+        free(L);
+        return MOE_ERR_CUDA;
+      }
+    } else if (!encode_bf16_2d(&L->tm_st_g, w->w_gate, c.d_model, G * c.d_ff, 16) ||
+               !encode_bf16_2d(&L->tm_st_u, w->w_up, c.d_model, G * c.d_ff, 16) ||
+               !encode_bf16_2d(&L->tm_st_d, w->w_down, c.d_ff, G * c.d_model, 16)) {
+      free(L);
+      return MOE_ERR_CUDA;
+    }
+    if (!mx && (!encode_bf16_2d(&L->tm_wg, w->w_gate, c.d_model, G * c.d_ff, kBM) ||
         !encode_bf16_2d(&L->tm_wu, w->w_up, c.d_model, G * c.d_ff, kBM) ||
         !encode_bf16_2d(&L->tm_wd, w->w_down, c.d_ff, G * c.d_model, kBM) ||
         !encode_bf16_2d(&L->tm_wr, w->w_router, c.d_model, c.n_experts, kBM) ||
@@ -752,7 +800,7 @@ static moe_status layer_init(const moe_config *cfg, const moe_weights *w, int e0
                          (uint32_t)router_half_tile(c))) ||
         !encode_bf16_2d(&L->tm_wg_mn, w->w_gate, c.d_model, G * c.d_ff, 64) ||
         !encode_bf16_2d(&L->tm_wu_mn, w->w_up, c.d_model, G * c.d_ff, 64) ||
-        !encode_bf16_2d(&L->tm_wd_mn, w->w_down, c.d_ff, G * c.d_model, 64)) {
+        !encode_bf16_2d(&L->tm_wd_mn, w->w_down, c.d_ff, G * c.d_model, 64))) {
       free(L);
       return MOE_ERR_CUDA;
     }
@@ -769,6 +817,18 @@ moe_status moe_layer_init_ep(const moe_config *cfg, const moe_weights *w, int ex
                              int expert_end, moe_handle *out) {
   if (cfg && cfg->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   return layer_init(cfg, w, expert_begin, expert_end, out);
+}
+
+moe_status moe_layer_init_mxfp4(const moe_config *cfg, const moe_mxfp4_weights *w,
+                                moe_handle *out) {
+  if (!cfg || !w || !out) return MOE_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (cfg->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!w->scale_gate || !w->scale_up || !w->scale_down) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w->scale_gate) || !aligned16(w->scale_up) || !aligned16(w->scale_down))
+    return MOE_ERR_ALIGNMENT;
+  const moe_weights codes{w->w_router, w->router_bias, w->w_gate, w->w_up, w->w_down};
+  return layer_init(cfg, &codes, 0, cfg->n_experts, out, w);
 }
 
 moe_status moe_layer_destroy(moe_handle h) {
@@ -813,7 +873,7 @@ moe_status moe_set_option(moe_handle h, int option, int value) {
 
 size_t moe_workspace_size(moe_handle h, int n_tokens) {
   if (!h || n_tokens < 0 || n_tokens > h->cfg.max_tokens) return 0;
-  return ws_layout(h->cfg, n_tokens < 1 ? 1 : n_tokens).total;
+  return ws_layout(h->cfg, n_tokens < 1 ? 1 : n_tokens, h->mx != 0).total;
 }
 
 moe_status moe_workspace_init(moe_handle h, void *ws, size_t ws_bytes, void *stream) {
@@ -884,7 +944,8 @@ static moe_status backward_entry(moe_handle h, const void *x, int n_tokens, cons
                                  float *dw_down, void *ws, size_t ws_bytes, void *stream) {
   if (!h) return MOE_ERR_INVALID_ARG;
   if (n_tokens < 0 || n_tokens > h->cfg.max_tokens) return MOE_ERR_INVALID_ARG;
-  if (!holds_all_experts(h)) return MOE_ERR_UNSUPPORTED;  // an expert-parallel slice
+  // an expert-parallel slice, or MXFP4 weights (which are not trained)
+  if (!holds_all_experts(h) || h->mx) return MOE_ERR_UNSUPPORTED;
   if (n_tokens == 0) return MOE_OK;
   if (!x || !dout || !dx || !dw_router || !dw_gate || !dw_up || !dw_down)
     return MOE_ERR_INVALID_ARG;
@@ -916,7 +977,7 @@ moe_status moe_expert_health(moe_handle h, int n_tokens, float *act_rms, float *
                              float *ratios, void *ws, size_t ws_bytes, void *stream) {
   moe_status s = check_call(h, n_tokens, ws, ws_bytes);
   if (s != MOE_OK) return s;
-  if (!holds_all_experts(h)) return MOE_ERR_UNSUPPORTED;  // an expert-parallel slice
+  if (!holds_all_experts(h) || h->mx) return MOE_ERR_UNSUPPORTED;  // a slice, MXFP4 weights
   if (n_tokens == 0 || !act_rms || !param_norm || !ratios) return MOE_ERR_INVALID_ARG;
   const moe_config &c = h->cfg;
   const int T = n_tokens, Tk = T * c.top_k, G = c.n_experts + c.n_shared;
@@ -1328,12 +1389,126 @@ moe_status launch_shared_side(const moe_layer *h, const void *x, int T, void *ws
   if ((s = launch_gemm_pair<MODE_DOWN>(h, p2, sd, h->side_sms)) != MOE_OK) return s;
   return cudaEventRecord(h->ev_join, sd) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
+// ------------------------------------------------------------------ weight streaming
+// The one-launch layer: at most 64 tokens and 512 (token, slot) pairs, and the decode router's
+// limits (every CTA selects for all tokens).
+bool few_ok(const moe_layer *L, int T) {
+  const moe_config &c = L->cfg;
+  return decode_route_ok(c, T) && T <= kStreamMaxT && T * c.top_k <= kStreamMaxPairs;
+}
+
+template <bool kMx, int NT, bool kRoute>
+moe_status launch_stream(const moe_layer *L, const StreamParams &p, cudaStream_t st) {
+  constexpr size_t smem = StreamCfg<kMx, NT>::SMEM;
+  if (smem > (size_t)L->smem_optin) return MOE_ERR_UNSUPPORTED;
+  auto kern = weight_stream_kernel<kMx, NT, kRoute>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess)
+    return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(L->num_sms);
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  if (kRoute) {  // its CTAs meet at a barrier of the grid: all must be resident at once
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+StreamParams stream_params(const moe_layer *L, const void *x, int T, void *out, void *ws,
+                           const WsLayout &W) {
+  const moe_config &c = L->cfg;
+  StreamParams p;
+  memset(&p, 0, sizeof p);
+  p.tm_g = L->tm_st_g;
+  p.tm_u = L->tm_st_u;
+  p.tm_d = L->tm_st_d;
+  p.sc_g = L->sc_gate;
+  p.sc_u = L->sc_up;
+  p.sc_d = L->sc_down;
+  p.x = static_cast<const __nv_bfloat16 *>(x);
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.xq = at<uint8_t>(ws, W.xq);
+  p.hq = at<uint8_t>(ws, W.hq);
+  p.h = at<__nv_bfloat16>(ws, W.h);
+  p.y = at<float>(ws, W.y);
+  p.offsets = at<int>(ws, W.offsets);
+  p.perm = at<int>(ws, W.perm);
+  p.slot_row = at<int>(ws, W.slot_row);
+  p.gate = at<float>(ws, W.gate);
+  p.w_router = static_cast<const __nv_bfloat16 *>(L->w.w_router);
+  p.bias = L->w.router_bias;
+  p.logits = at<float>(ws, W.logits);
+  p.done = at<int>(ws, W.done);
+  p.tile_done = p.done + c.n_experts + c.n_shared;
+  p.status = at<DevStatus>(ws, W.status);
+  p.sched = &p.status->sched[0];
+  p.grid_bar = p.status->grid_bar;
+  p.T = T;
+  p.d = c.d_model;
+  p.f = c.d_ff;
+  p.E = c.n_experts;
+  p.k = c.top_k;
+  p.n_shared = c.n_shared;
+  p.routed_scale = c.routed_scale;
+  return p;
+}
+
+// The whole layer in one launch (few_ok).
+moe_status forward_few(const moe_layer *L, const void *x, int T, void *out, void *ws,
+                       cudaStream_t st) {
+  const StreamParams p = stream_params(L, x, T, out, ws, ws_layout(L->cfg, T, L->mx != 0));
+  if (L->mx)
+    return T <= 8 ? launch_stream<true, 1, true>(L, p, st) : launch_stream<true, 2, true>(L, p, st);
+  return T <= 8 ? launch_stream<false, 1, true>(L, p, st) : launch_stream<false, 2, true>(L, p, st);
+}
+
+// moe_forward of an MXFP4 handle.
+moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, void *ws,
+                         cudaStream_t st) {
+  if (few_ok(L, T)) return forward_few(L, x, T, out, ws, st);
+  const moe_config &c = L->cfg;
+  const WsLayout W = ws_layout(c, T, true);
+  DevStatus *status = at<DevStatus>(ws, W.status);
+  const CounterReset reset{status->sched, at<int>(ws, W.done),
+                           c.n_experts + c.n_shared + c.d_model / kStreamMinTile};
+  float *logits = at<float>(ws, W.logits);
+  moe_status s;
+  if ((s = launch_logits(L, x, T, logits, at<float>(ws, W.part), status, st)) != MOE_OK ||
+      (s = launch_select_permute(L, logits, T, nullptr, at<int>(ws, W.idx),
+                                 at<float>(ws, W.gate), at<int>(ws, W.counts),
+                                 at<int>(ws, W.offsets), at<int>(ws, W.perm),
+                                 at<int>(ws, W.slot_row), at<int>(ws, W.chunk_hist), reset,
+                                 st)) != MOE_OK ||
+      (s = launch(act_block_scale_kernel,
+                  dim3(grid_for((size_t)T * c.d_model / kMxPerLane, 256, L->num_sms)), dim3(256),
+                  0, st, static_cast<const __nv_bfloat16 *>(x), T, c.d_model,
+                  at<uint8_t>(ws, W.xq))) != MOE_OK)
+    return s;
+  return launch_stream<true, 2, false>(L, stream_params(L, x, T, out, ws, W), st);
+}
+
+int mxfp4_launches(const moe_layer *L, int T) {
+  if (T == 0) return 0;
+  if (few_ok(L, T)) return 1;
+  return (T <= kChunk ? 2 : 3) + 2;
+}
 }  // namespace
 
 extern "C" {
 
 int moe_forward_launch_count(moe_handle h, int n_tokens) {
   if (!h || n_tokens < 0 || n_tokens > h->cfg.max_tokens) return -1;
+  if (h->mx) return mxfp4_launches(h, n_tokens);
   return plan_forward(h, n_tokens).launches;
 }
 
@@ -1346,6 +1521,10 @@ static moe_status forward_impl(moe_handle h, const void *x, int n_tokens, void *
   if (n_tokens == 0) return MOE_OK;
   if (!x || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(out)) return MOE_ERR_ALIGNMENT;
+  if (h->mx) {
+    if (events || saved) return MOE_ERR_UNSUPPORTED;
+    return forward_mxfp4(h, x, n_tokens, out, ws, static_cast<cudaStream_t>(stream));
+  }
   const moe_config &c = h->cfg;
   const int T = n_tokens;
   const int Tk = T * c.top_k;
@@ -1463,6 +1642,62 @@ moe_status moe_forward_save(moe_handle h, const void *x, int n_tokens, void *out
 moe_status moe_forward(moe_handle h, const void *x, int n_tokens, void *out, void *ws,
                        size_t ws_bytes, void *stream) {
   return forward_impl(h, x, n_tokens, out, ws, ws_bytes, stream, nullptr);
+}
+
+moe_status moe_forward_few(moe_handle h, const void *x, int n_tokens, void *out, void *ws,
+                           size_t ws_bytes, void *stream) {
+  moe_status s = check_call(h, n_tokens, ws, ws_bytes);
+  if (s != MOE_OK) return s;
+  if (!holds_all_experts(h)) return MOE_ERR_UNSUPPORTED;  // an expert-parallel slice
+  if (n_tokens == 0) return MOE_OK;
+  if (!few_ok(h, n_tokens)) return MOE_ERR_UNSUPPORTED;
+  if (!x || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(out)) return MOE_ERR_ALIGNMENT;
+  return forward_few(h, x, n_tokens, out, ws, static_cast<cudaStream_t>(stream));
+}
+
+static bool mxfp4_args(const void *m, moe_dtype dtype, long long rows, int cols,
+                       const uint8_t *codes, const uint8_t *scales, moe_status *s) {
+  *s = MOE_ERR_INVALID_ARG;
+  if (rows < 0 || cols < 0 || cols % kMxBlock != 0 || (dtype != MOE_F32 && dtype != MOE_BF16))
+    return false;
+  *s = MOE_OK;
+  if (rows == 0 || cols == 0) return false;  // nothing to do
+  *s = MOE_ERR_INVALID_ARG;
+  if (!m || !codes || !scales || rows > (1ll << 62) / cols / 4) return false;
+  *s = MOE_ERR_ALIGNMENT;
+  return aligned16(m) && aligned16(codes);
+}
+
+static dim3 mxfp4_grid(size_t lanes) {  // 256 threads; enough blocks to fill the device
+  const size_t b = (lanes + 255) / 256;
+  return dim3((unsigned)(b < 148 * 8 ? b : 148 * 8));
+}
+
+moe_status moe_mxfp4_quantize(const void *src, moe_dtype dtype, long long rows, int cols,
+                              uint8_t *codes, uint8_t *scales, void *stream) {
+  moe_status s;
+  if (!mxfp4_args(src, dtype, rows, cols, codes, scales, &s)) return s;
+  const size_t lanes = (size_t)rows * cols / kMxPerLane;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == MOE_BF16)
+    return launch(mxfp4_quantize_kernel<__nv_bfloat16>, mxfp4_grid(lanes), dim3(256), 0, st,
+                  static_cast<const __nv_bfloat16 *>(src), lanes, codes, scales);
+  return launch(mxfp4_quantize_kernel<float>, mxfp4_grid(lanes), dim3(256), 0, st,
+                static_cast<const float *>(src), lanes, codes, scales);
+}
+
+moe_status moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, long long rows,
+                                int cols, void *dst, moe_dtype dtype, void *stream) {
+  moe_status s;
+  if (!mxfp4_args(dst, dtype, rows, cols, codes, scales, &s)) return s;
+  const size_t lanes = (size_t)rows * cols / kMxPerLane;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (dtype == MOE_BF16)
+    return launch(mxfp4_dequantize_kernel<__nv_bfloat16>, mxfp4_grid(lanes), dim3(256), 0, st,
+                  codes, scales, lanes, static_cast<__nv_bfloat16 *>(dst));
+  return launch(mxfp4_dequantize_kernel<float>, mxfp4_grid(lanes), dim3(256), 0, st, codes,
+                scales, lanes, static_cast<float *>(dst));
 }
 
 moe_status moe_forward_profiled(moe_handle h, const void *x, int n_tokens, void *out,

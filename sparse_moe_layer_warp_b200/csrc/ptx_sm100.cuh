@@ -23,7 +23,9 @@ struct DevStatus {
   // bf16 expert GEMMs with MOE_OPTION_GEMM_CLOCK: SM cycles and %globaltimer ns from entry to
   // exit of every CTA, summed ([0], [1] up; [2], [3] down), read and cleared by moe_gemm_clock
   unsigned long long gemm_clock[4];
-  int pad[12];
+  int grid_bar[2];       // one-launch layer: arrivals at and departures from its grid barrier
+                         // (cleared by the last CTA to leave)
+  int pad[10];
   int router_ticket[32]; // split-K router: arrivals per block of 32 experts; [31] also the
                          // decode router's last-CTA ticket (all self-resetting)
 };

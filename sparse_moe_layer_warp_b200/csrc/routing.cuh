@@ -469,85 +469,105 @@ __device__ __forceinline__ float dot8_bf16(const uint4 a, const uint4 b) {
   return s;
 }
 
+// Router weights of experts e0, e0 + 1 in the registers of kDecodeWarps warps (a K slice each).
+constexpr int kDecodeMaxC = kDecodeMaxD / (kDecodeWarps * 8) / 32;
+__device__ __forceinline__ void decode_load_router_rows(const __nv_bfloat16 *__restrict__ wr, int e0,
+                                                        int d, int E,
+                                                        uint4 (&w)[kDecodeMaxC][kDecodeEPC]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slice = d / kDecodeWarps;  // this warp's K range
+  const int chunks = slice / 8;        // 16-byte chunks in it
+#pragma unroll
+  for (int ci = 0; ci < kDecodeMaxC; ++ci) {
+    const int c = lane + 32 * ci;
+#pragma unroll
+    for (int e = 0; e < kDecodeEPC; ++e) {
+      w[ci][e] = make_uint4(0u, 0u, 0u, 0u);
+      if (warp < kDecodeWarps && c < chunks && e0 + e < E)
+        w[ci][e] = __ldg(reinterpret_cast<const uint4 *>(wr + (size_t)(e0 + e) * d +
+                                                         warp * slice + c * 8));
+    }
+  }
+}
+
+// Their logits for all T tokens.  Called by the whole CTA (kDecodeWarps warps or more, which only
+// take part in the barriers); red: kDecodeWarps x 32 floats of shared memory.
+__device__ __forceinline__ void decode_router_rows(const __nv_bfloat16 *__restrict__ x, int e0,
+                                                   int T, int d, int E,
+                                                   const uint4 (&w)[kDecodeMaxC][kDecodeEPC],
+                                                   float *__restrict__ logits, float *red) {
+  constexpr int EPC = kDecodeEPC, TG = 16, NW = kDecodeWarps;
+  static_assert(EPC * TG == 32, "one butterfly value per lane");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int slice = d / NW, chunks = slice / 8;
+  for (int tg = 0; tg < T; tg += TG) {
+    if (warp < NW) {
+      float a[EPC * TG];  // value j = e * TG + t
+#pragma unroll
+      for (int j = 0; j < EPC * TG; ++j) a[j] = 0.f;
+      // tokens past T read token T-1 (clamped, so the loads are unconditional and issue
+      // together); their sums are never stored
+#pragma unroll
+      for (int ci = 0; ci < kDecodeMaxC; ++ci) {
+        const int c = lane + 32 * ci;
+        if (ci * 32 < chunks) {  // warp-uniform
+          const int cc = min(c, chunks - 1);
+#pragma unroll
+          for (int t0 = 0; t0 < TG; t0 += 8) {
+            uint4 xv[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              xv[t] = __ldg(reinterpret_cast<const uint4 *>(
+                  x + (size_t)min(tg + t0 + t, T - 1) * d + warp * slice + cc * 8));
+            if (c < chunks) {
+#pragma unroll
+              for (int t = 0; t < 8; ++t)
+#pragma unroll
+                for (int e = 0; e < EPC; ++e) a[e * TG + t0 + t] += dot8_bf16(xv[t], w[ci][e]);
+            }
+          }
+        }
+      }
+      // butterfly: after the step with offset o a lane keeps the half of its 2o values whose
+      // index bit matches its lane bit, so lane j ends with the warp's sum of value j
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+        const bool upper = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+          const float send = upper ? a[i] : a[i + o];
+          const float keep = upper ? a[i + o] : a[i];
+          a[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      }
+      red[warp * 32 + lane] = a[0];
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      float v = 0.f;
+#pragma unroll
+      for (int ww = 0; ww < NW; ++ww) v += red[ww * 32 + threadIdx.x];
+      const int e = threadIdx.x / TG, t = threadIdx.x % TG;
+      if (tg + t < T && e0 + e < E) logits[(size_t)(tg + t) * E + e0 + e] = v;
+    }
+    __syncthreads();
+  }
+}
+
 __global__ void __launch_bounds__(kDecodeWarps * 32) route_decode_kernel(
     const __nv_bfloat16 *__restrict__ x, const __nv_bfloat16 *__restrict__ wr,
     const float *__restrict__ bias, int T, int d, int E, int k, float *__restrict__ logits,
     int *__restrict__ topk_idx, float *__restrict__ topk_gate, int *__restrict__ counts,
     int *__restrict__ offsets, int *__restrict__ perm, int *__restrict__ slot_row,
     int *__restrict__ ticket, CounterReset reset) {
-  constexpr int EPC = kDecodeEPC, TG = 16, NW = kDecodeWarps;
-  constexpr int MAXC = kDecodeMaxD / (NW * 8) / 32;
-  static_assert(EPC * TG == 32, "one butterfly value per lane");
-  __shared__ float red[NW][32];
+  __shared__ float red[kDecodeWarps * 32];
   __shared__ int s_last;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int e0 = blockIdx.x * EPC;
-  const int slice = d / NW;        // this warp's K range
-  const int chunks = slice / 8;    // 16-byte chunks in it
-  uint4 w[MAXC][EPC];
-#pragma unroll
-  for (int ci = 0; ci < MAXC; ++ci) {
-    const int c = lane + 32 * ci;
-#pragma unroll
-    for (int e = 0; e < EPC; ++e) {
-      w[ci][e] = make_uint4(0u, 0u, 0u, 0u);
-      if (c < chunks && e0 + e < E)
-        w[ci][e] = __ldg(reinterpret_cast<const uint4 *>(wr + (size_t)(e0 + e) * d +
-                                                         warp * slice + c * 8));
-    }
-  }
+  const int e0 = blockIdx.x * kDecodeEPC;
+  uint4 w[kDecodeMaxC][kDecodeEPC];
+  decode_load_router_rows(wr, e0, d, E, w);
   griddep_wait();
   griddep_launch_dependents();
-  for (int tg = 0; tg < T; tg += TG) {
-    float a[EPC * TG];  // value j = e * TG + t
-#pragma unroll
-    for (int j = 0; j < EPC * TG; ++j) a[j] = 0.f;
-    // tokens past T read token T-1 (clamped, so the loads are unconditional and issue
-    // together); their sums are never stored
-#pragma unroll
-    for (int ci = 0; ci < MAXC; ++ci) {
-      const int c = lane + 32 * ci;
-      if (ci * 32 < chunks) {  // warp-uniform
-        const int cc = min(c, chunks - 1);
-#pragma unroll
-        for (int t0 = 0; t0 < TG; t0 += 8) {
-          uint4 xv[8];
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-            xv[t] = __ldg(reinterpret_cast<const uint4 *>(
-                x + (size_t)min(tg + t0 + t, T - 1) * d + warp * slice + cc * 8));
-          if (c < chunks) {
-#pragma unroll
-            for (int t = 0; t < 8; ++t)
-#pragma unroll
-              for (int e = 0; e < EPC; ++e) a[e * TG + t0 + t] += dot8_bf16(xv[t], w[ci][e]);
-          }
-        }
-      }
-    }
-    // butterfly: after the step with offset o a lane keeps the half of its 2o values whose
-    // index bit matches its lane bit, so lane j ends with the warp's sum of value j
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      const bool upper = (lane & o) != 0;
-#pragma unroll
-      for (int i = 0; i < o; ++i) {
-        const float send = upper ? a[i] : a[i + o];
-        const float keep = upper ? a[i + o] : a[i];
-        a[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-      }
-    }
-    red[warp][lane] = a[0];
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      float v = 0.f;
-#pragma unroll
-      for (int ww = 0; ww < NW; ++ww) v += red[ww][threadIdx.x];
-      const int e = threadIdx.x / TG, t = threadIdx.x % TG;
-      if (tg + t < T && e0 + e < E) logits[(size_t)(tg + t) * E + e0 + e] = v;
-    }
-    __syncthreads();
-  }
+  decode_router_rows(x, e0, T, d, E, w, logits, red);
   // the last CTA to finish its experts routes all tokens
   __threadfence();
   __syncthreads();

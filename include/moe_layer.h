@@ -109,17 +109,26 @@ moe_status moe_layer_init(const moe_config *cfg, const moe_weights *w, moe_handl
  * moe_mxfp4_dequantize: the values, fp32 or bf16 (dst 16-byte aligned).  Exact in both types for
  * bytes up to 252, the largest that moe_mxfp4_quantize writes; above, a code whose value is past
  * the type's range becomes infinite.
- * Both are asynchronous on `stream` and need no handle; rows or cols of 0 do nothing;
- * MOE_ERR_INVALID_ARG for a null pointer, negative size, cols not a multiple of 32 or unknown
- * dtype. */
+ * moe_mxfp4_tile_scales: scales [rows, cols / 32] (rows and cols multiples of 128) in the order in
+ * which the layer's kernels load them, tiled (as many bytes); both 16-byte aligned.  Blocks of 512
+ * bytes for 128 rows x 128 columns, with nb = cols / 32:
+ *   tiled[(r / 128 * (nb / 4) + b / 4) * 512 + r % 32 * 16 + r % 128 / 32 * 4 + b % 4]
+ *     = scales[r * nb + b].
+ * All three are asynchronous on `stream` and need no handle; rows or cols of 0 do nothing;
+ * MOE_ERR_INVALID_ARG for a null pointer, a negative size, cols not a multiple of 32, rows or cols
+ * to tile not multiples of 128, or an unknown dtype. */
 moe_status moe_mxfp4_quantize(const void *src, moe_dtype dtype, long long rows, int cols,
                               uint8_t *codes, uint8_t *scales, void *stream);
 moe_status moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, long long rows,
                                 int cols, void *dst, moe_dtype dtype, void *stream);
 
+moe_status moe_mxfp4_tile_scales(const uint8_t *scales, long long rows, int cols, uint8_t *tiled,
+                                 void *stream);
+
 /* Caller-owned device pointers of a layer whose expert weights are MXFP4: the router as in
  * moe_weights (bf16), the codes of w_gate, w_up [G, f, d / 2] and w_down [G, d, f / 2], and their
- * scales [G, f, d / 32] and [G, d, f / 32], every pointer 16-byte aligned. */
+ * scales as moe_mxfp4_tile_scales orders them (of the G * f rows of w_gate and w_up and the G * d
+ * rows of w_down), every pointer 16-byte aligned, the codes 32-byte aligned. */
 typedef struct {
   const void *w_router;
   const float *router_bias; /* may be null: zero bias */

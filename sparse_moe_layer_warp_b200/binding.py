@@ -35,7 +35,7 @@ EXPORTS = ("moe_layer_init", "moe_layer_destroy", "moe_workspace_size", "moe_wor
            "moe_backward_saved", "moe_backward_ex", "moe_set_option", "moe_layer_init_ep",
            "moe_forward_partial", "moe_ep_plan", "moe_ep_pack", "moe_ep_combine",
            "moe_gemm_clock", "moe_mxfp4_quantize", "moe_mxfp4_dequantize",
-           "moe_layer_init_mxfp4", "moe_forward_few")
+           "moe_mxfp4_tile_scales", "moe_layer_init_mxfp4", "moe_forward_few")
 MXFP4_BLOCK = 32  # values that share a scale
 MOE_BACKWARD_OVERWRITE = 1
 MOE_OPTION_H_HANDOVER = 1
@@ -118,6 +118,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.moe_ep_combine.argtypes = [P, P, P, P, P, I, I, P, P]
         lib.moe_mxfp4_quantize.argtypes = [P, I, ctypes.c_longlong, I, P, P, P]
         lib.moe_mxfp4_dequantize.argtypes = [P, P, ctypes.c_longlong, I, P, I, P]
+        lib.moe_mxfp4_tile_scales.argtypes = [P, ctypes.c_longlong, I, P, P]
         lib.moe_layer_init_mxfp4.argtypes = [ctypes.POINTER(moe_config),
                                              ctypes.POINTER(moe_mxfp4_weights),
                                              ctypes.POINTER(P)]
@@ -134,7 +135,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                      "moe_backward_saved", "moe_backward_ex", "moe_set_option", "moe_layer_init_ep",
                      "moe_forward_partial", "moe_ep_plan", "moe_ep_pack", "moe_ep_combine",
                      "moe_gemm_clock", "moe_mxfp4_quantize", "moe_mxfp4_dequantize",
-                     "moe_layer_init_mxfp4", "moe_forward_few"):
+                     "moe_mxfp4_tile_scales", "moe_layer_init_mxfp4", "moe_forward_few"):
             getattr(lib, name).restype = I
         _lib = lib
     return _lib
@@ -196,7 +197,8 @@ def moe_layer_init_ep(cfg: moe_config, expert_begin: int, expert_end: int, w_rou
 
 
 def moe_layer_init_mxfp4(cfg: moe_config, w_router, router_bias, w_gate, w_up, w_down):
-    """Handle of a layer over MXFP4 expert weights: w_gate, w_up, w_down are (codes, scales)."""
+    """Handle of a layer over MXFP4 expert weights: w_gate, w_up, w_down are (codes, tiled
+    scales)."""
     lib = load_library()
     w = moe_mxfp4_weights(_addr(w_router), None if router_bias is None else _addr(router_bias),
                           *(_addr(t[0]) for t in (w_gate, w_up, w_down)),
@@ -301,6 +303,13 @@ def moe_mxfp4_dequantize(codes, scales, dst, stream=None) -> None:
     _check("moe_mxfp4_dequantize", load_library().moe_mxfp4_dequantize(
         _p(codes), _p(scales), dst.numel() // max(cols, 1), cols, _p(dst),
         _DTYPE_CODE[dst.dtype], _stream(stream)))
+
+
+def moe_mxfp4_tile_scales(scales, tiled, stream=None) -> None:
+    """`scales` [.., rows, cols / 32] in the order in which the layer's kernels load them."""
+    kb = int(scales.shape[-1])
+    _check("moe_mxfp4_tile_scales", load_library().moe_mxfp4_tile_scales(
+        _p(scales), scales.numel() // max(kb, 1), kb * MXFP4_BLOCK, _p(tiled), _stream(stream)))
 
 
 def moe_backward_workspace_size(handle, n_tokens: int) -> int:
@@ -680,8 +689,8 @@ class MoELayer:
 
 class MoELayerMXFP4(MoELayer):
     """MoELayer over MXFP4 expert weights, for serving: w_gate, w_up [E + n_shared, f, d] and
-    w_down [E + n_shared, d, f] are (codes, scales) as mxfp4_quantize returns them; the router and
-    the activations are bf16.  forward, forward_few, route and router_stats as in MoELayer;
+    w_down [E + n_shared, d, f] are (codes, scales) as mxfp4_quantize returns them (the layer keeps
+    the codes and a tiled copy of the scales); the router and the activations are bf16.  forward, forward_few, route and router_stats as in MoELayer;
     training calls and expert_health are refused by the library (MoEError)."""
 
     def __init__(self, w_router, router_bias, w_gate, w_up, w_down, top_k: int,
@@ -703,7 +712,13 @@ class MoELayerMXFP4(MoELayer):
         self.cfg = moe_config(int(max_tokens), int(d), int(E), int(top_k), int(f),
                               int(n_shared), MOE_BF16, float(routed_scale))
         self.handle = None
-        self.tensors = (w_router, router_bias, tuple(w_gate), tuple(w_up), tuple(w_down))
+        tiled = []
+        with torch.cuda.device(w_router.device):
+            for codes, scales in (w_gate, w_up, w_down):
+                t = torch.empty_like(scales)
+                moe_mxfp4_tile_scales(scales, t)
+                tiled.append((codes, t))
+        self.tensors = (w_router, router_bias, *tiled)
         self.handle = moe_layer_init_mxfp4(self.cfg, *self.tensors)
         self.device = w_router.device
         self.dtype = w_router.dtype

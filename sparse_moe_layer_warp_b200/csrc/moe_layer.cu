@@ -33,6 +33,7 @@
 #include "grouped_gemm_bw.cuh"
 #include "grouped_gemm_pair.cuh"
 #include "mxfp4.cuh"
+#include "mxfp4_layer.cuh"
 #include "ptx_sm100.cuh"
 #include "router_stats.cuh"
 #include "routing.cuh"
@@ -130,8 +131,23 @@ bool encode_f32_2d(CUtensorMap *m, void *base, uint64_t cols, uint64_t rows) {
          CUDA_SUCCESS;
 }
 
-// Row-major bytes [rows, cols] -> tiled map with box {128 bytes, box_rows rows} and 128-byte
-// swizzle (MXFP4 codes: 256 columns of K a box row).
+// MXFP4 codes [rows, cols] (two a byte) -> map with box {128 codes, 128 rows}: in shared memory one
+// byte a code (8 bytes of codes, 8 of padding), 128-byte swizzle.  The padded format wants 32-byte
+// alignment and cols a multiple of 128.
+bool encode_codes(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols / 2};
+  cuuint32_t box[2] = {128, kMxTile};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void *>(base), dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// Row-major bytes [rows, cols] -> map with box {128 bytes, box_rows rows} and 128-byte swizzle.
 bool encode_u8_2d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows,
                   uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
@@ -142,6 +158,22 @@ bool encode_u8_2d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows
   cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// Row-major bf16 matrix [rows, cols] seen as [cols / 64][rows][64] -> map with box {64 columns,
+// box_rows rows, 4 column groups}: one load fills four 128-byte-swizzled tiles of box_rows rows.
+bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows,
+                    uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {64, rows, cols / 64};
+  cuuint64_t strides[2] = {cols * 2, 128};
+  cuuint32_t box[3] = {64, box_rows, 4};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
@@ -199,10 +231,11 @@ size_t esize(const moe_config &c) { return c.dtype == MOE_BF16 ? 2 : 4; }
 // Workspace regions (256-byte aligned).  P = T*k + n_shared*T rows of the sorted space.
 struct WsLayout {
   size_t status, logits, part, idx, gate, counts, offsets, perm, slot_row, chunk_hist, stats,
-      xs, h, y, done, health, xq, hq, total;
+      xs, h, y, done, health, x_split, x_scale, h_scale, total;
 };
 
 int pick_bn(const moe_config &c, int T, int mode);
+bool decode_route_ok(const moe_config &c, int T);
 
 // The bf16 up GEMM gathers its token rows from x when its token tile is small; larger
 // tiles read an expert-sorted copy xs written by gather_rows_by_token_kernel.
@@ -210,7 +243,14 @@ bool up_gathers_rows(const moe_config &c, int T) {
   return pick_bn(c, T, MODE_UP) <= kGatherMaxBN;
 }
 
-// mx: an MXFP4 handle's layout (block-scaled fp16 x and h of the weight-streaming kernel)
+// The one-launch layer: at most 64 tokens and 512 (token, slot) pairs, and the decode router's
+// limits (every CTA selects for all tokens).
+bool few_shape(const moe_config &c, int T) {
+  return decode_route_ok(c, T) && T <= kStreamMaxT && T * c.top_k <= kStreamMaxPairs;
+}
+
+// mx: an MXFP4 handle's layout (x and h as pairs of e4m3 values with their scales; x by token for
+// the one-launch layer, by sorted row otherwise)
 WsLayout ws_layout(const moe_config &c, int T, bool mx = false) {
   WsLayout L;
   size_t off = 0;
@@ -235,15 +275,17 @@ WsLayout ws_layout(const moe_config &c, int T, bool mx = false) {
   L.slot_row = take(Tk * 4);
   L.chunk_hist = take(nch * ((size_t)c.n_experts + kMaxTopK) * 4);
   L.stats = take(nch * (2 * (size_t)c.n_experts + 1) * 4);  // router statistics partials
-  L.xs = (c.dtype == MOE_BF16 && !up_gathers_rows(c, T)) ? take(Tk * c.d_model * 2) : off;
+  L.xs = (c.dtype == MOE_BF16 && !mx && !up_gathers_rows(c, T)) ? take(Tk * c.d_model * 2) : off;
   L.h = take(P * c.d_ff * esize(c));
   L.y = take(P * c.d_model * 4);  // fp32 in both precisions
-  // per-group up completion counts, then the weight-streaming kernel's per-tile y counts
-  L.done = take(((size_t)c.n_experts + c.n_shared + c.d_model / kStreamMinTile) * 4);
+  // per-group up completion counts, then the weight-streaming kernel's: all groups, y tiles
+  L.done = take(((size_t)c.n_experts + c.n_shared + 1 + c.d_model / kStreamMinTile) * 4);
   // expert health: slice sums of squares, activations then parameters
   L.health = take(2 * ((size_t)c.n_experts + c.n_shared) * kHealthSlices * 8);
-  L.xq = take(mx ? (size_t)T * act_chunks(c.d_model) * kActChunkBytes : 0);
-  L.hq = take(mx ? P * act_chunks(c.d_ff) * kActChunkBytes : 0);
+  const size_t x_rows = !mx ? 0 : few_shape(c, T) ? (size_t)T : P;
+  L.x_split = take(2 * x_rows * c.d_model);
+  L.x_scale = take(2 * x_rows * act_scale_ld(c.d_model));
+  L.h_scale = take(mx ? 2 * P * act_scale_ld(c.d_ff) : 0);
   L.total = off;
   return L;
 }
@@ -775,9 +817,9 @@ static moe_status layer_init(const moe_config *cfg, const moe_weights *w, int e0
       L->sc_gate = mx->scale_gate;
       L->sc_up = mx->scale_up;
       L->sc_down = mx->scale_down;
-      if (!encode_u8_2d(&L->tm_st_g, w->w_gate, c.d_model / 2, G * c.d_ff, 32) ||
-          !encode_u8_2d(&L->tm_st_u, w->w_up, c.d_model / 2, G * c.d_ff, 32) ||
-          !encode_u8_2d(&L->tm_st_d, w->w_down, c.d_ff / 2, G * c.d_model, 32) ||
+      if (!encode_codes(&L->tm_st_g, w->w_gate, c.d_model, G * c.d_ff) ||
+          !encode_codes(&L->tm_st_u, w->w_up, c.d_model, G * c.d_ff) ||
+          !encode_codes(&L->tm_st_d, w->w_down, c.d_ff, G * c.d_model) ||
           !encode_bf16_2d(&L->tm_wr, w->w_router, c.d_model, c.n_experts, kBM) ||
           (router_half_tile(c) &&
            !encode_bf16_2d(&L->tm_wr2, w->w_router, c.d_model, c.n_experts,
@@ -785,9 +827,9 @@ static moe_status layer_init(const moe_config *cfg, const moe_weights *w, int e0
         free(L);
         return MOE_ERR_CUDA;
       }
-    } else if (!encode_bf16_2d(&L->tm_st_g, w->w_gate, c.d_model, G * c.d_ff, 16) ||
-               !encode_bf16_2d(&L->tm_st_u, w->w_up, c.d_model, G * c.d_ff, 16) ||
-               !encode_bf16_2d(&L->tm_st_d, w->w_down, c.d_ff, G * c.d_model, 16)) {
+    } else if (!encode_bf16_3d(&L->tm_st_g, w->w_gate, c.d_model, G * c.d_ff, 16) ||
+               !encode_bf16_3d(&L->tm_st_u, w->w_up, c.d_model, G * c.d_ff, 16) ||
+               !encode_bf16_3d(&L->tm_st_d, w->w_down, c.d_ff, G * c.d_model, 16)) {
       free(L);
       return MOE_ERR_CUDA;
     }
@@ -824,8 +866,14 @@ moe_status moe_layer_init_mxfp4(const moe_config *cfg, const moe_mxfp4_weights *
   if (!cfg || !w || !out) return MOE_ERR_INVALID_ARG;
   *out = nullptr;
   if (cfg->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  // counts of finished pieces of h are 32-bit
+  if (cfg->max_tokens > 0 && cfg->d_ff > 0 && cfg->top_k > 0 &&
+      (double)cfg->max_tokens * (cfg->top_k + 1) * (cfg->d_ff / 32) >= 2147483648.0)
+    return MOE_ERR_UNSUPPORTED;
   if (!w->scale_gate || !w->scale_up || !w->scale_down) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(w->scale_gate) || !aligned16(w->scale_up) || !aligned16(w->scale_down))
+  if (!aligned16(w->scale_gate) || !aligned16(w->scale_up) || !aligned16(w->scale_down) ||
+      ((reinterpret_cast<uintptr_t>(w->w_gate) | reinterpret_cast<uintptr_t>(w->w_up) |
+        reinterpret_cast<uintptr_t>(w->w_down)) & 31u) != 0)  // the padded 4-bit TMA format
     return MOE_ERR_ALIGNMENT;
   const moe_weights codes{w->w_router, w->router_bias, w->w_gate, w->w_up, w->w_down};
   return layer_init(cfg, &codes, 0, cfg->n_experts, out, w);
@@ -1390,29 +1438,23 @@ moe_status launch_shared_side(const moe_layer *h, const void *x, int T, void *ws
   return cudaEventRecord(h->ev_join, sd) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 // ------------------------------------------------------------------ weight streaming
-// The one-launch layer: at most 64 tokens and 512 (token, slot) pairs, and the decode router's
-// limits (every CTA selects for all tokens).
-bool few_ok(const moe_layer *L, int T) {
-  const moe_config &c = L->cfg;
-  return decode_route_ok(c, T) && T <= kStreamMaxT && T * c.top_k <= kStreamMaxPairs;
-}
-
-template <bool kMx, int NT, bool kRoute>
-moe_status launch_stream(const moe_layer *L, const StreamParams &p, cudaStream_t st) {
-  constexpr size_t smem = StreamCfg<kMx, NT>::SMEM;
+// A persistent kernel over every SM; one_launch: its CTAs meet at a barrier of the grid, so all must
+// be resident at once.
+template <typename Params>
+moe_status launch_stream(const moe_layer *L, void (*kern)(const Params), const Params &p,
+                         int threads, size_t smem, bool one_launch, cudaStream_t st) {
   if (smem > (size_t)L->smem_optin) return MOE_ERR_UNSUPPORTED;
-  auto kern = weight_stream_kernel<kMx, NT, kRoute>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(L->num_sms);
-  cfg.blockDim = dim3(kStreamThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
-  if (kRoute) {  // its CTAs meet at a barrier of the grid: all must be resident at once
+  if (one_launch) {
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
   } else {
@@ -1424,22 +1466,13 @@ moe_status launch_stream(const moe_layer *L, const StreamParams &p, cudaStream_t
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-StreamParams stream_params(const moe_layer *L, const void *x, int T, void *out, void *ws,
-                           const WsLayout &W) {
+StreamBase stream_base(const moe_layer *L, const void *x, int T, void *out, void *ws,
+                       const WsLayout &W) {
   const moe_config &c = L->cfg;
-  StreamParams p;
+  StreamBase p;
   memset(&p, 0, sizeof p);
-  p.tm_g = L->tm_st_g;
-  p.tm_u = L->tm_st_u;
-  p.tm_d = L->tm_st_d;
-  p.sc_g = L->sc_gate;
-  p.sc_u = L->sc_up;
-  p.sc_d = L->sc_down;
   p.x = static_cast<const __nv_bfloat16 *>(x);
   p.out = static_cast<__nv_bfloat16 *>(out);
-  p.xq = at<uint8_t>(ws, W.xq);
-  p.hq = at<uint8_t>(ws, W.hq);
-  p.h = at<__nv_bfloat16>(ws, W.h);
   p.y = at<float>(ws, W.y);
   p.offsets = at<int>(ws, W.offsets);
   p.perm = at<int>(ws, W.perm);
@@ -1449,7 +1482,8 @@ StreamParams stream_params(const moe_layer *L, const void *x, int T, void *out, 
   p.bias = L->w.router_bias;
   p.logits = at<float>(ws, W.logits);
   p.done = at<int>(ws, W.done);
-  p.tile_done = p.done + c.n_experts + c.n_shared;
+  p.done_all = p.done + c.n_experts + c.n_shared;
+  p.tile_done = p.done_all + 1;
   p.status = at<DevStatus>(ws, W.status);
   p.sched = &p.status->sched[0];
   p.grid_bar = p.status->grid_bar;
@@ -1463,25 +1497,69 @@ StreamParams stream_params(const moe_layer *L, const void *x, int T, void *out, 
   return p;
 }
 
-// The whole layer in one launch (few_ok).
+// MXFP4 layer, token tiles of BN rows.
+template <int BN, bool kRoute>
+moe_status launch_mx(const moe_layer *L, const void *x, int T, void *out, void *ws,
+                     const WsLayout &W, cudaStream_t st) {
+  const moe_config &c = L->cfg;
+  const size_t P = (size_t)T * (c.top_k + c.n_shared), x_rows = kRoute ? (size_t)T : P;
+  MxParams p;
+  memset(&p, 0, sizeof p);
+  p.b = stream_base(L, x, T, out, ws, W);
+  p.tm_g = L->tm_st_g;
+  p.tm_u = L->tm_st_u;
+  p.tm_d = L->tm_st_d;
+  p.sc_g = L->sc_gate;
+  p.sc_u = L->sc_up;
+  p.sc_d = L->sc_down;
+  p.x = split_rows(at<uint8_t>(ws, W.x_split), at<uint8_t>(ws, W.x_scale), x_rows, c.d_model);
+  p.h = split_rows(at<uint8_t>(ws, W.h), at<uint8_t>(ws, W.h_scale), P, c.d_ff);
+  if (!kRoute && (!encode_u8_2d(&p.tm_xhi, p.x.hi, c.d_model, P, BN) ||
+                  !encode_u8_2d(&p.tm_xlo, p.x.lo, c.d_model, P, BN) ||
+                  !encode_u8_2d(&p.tm_hhi, p.h.hi, c.d_ff, P, BN) ||
+                  !encode_u8_2d(&p.tm_hlo, p.h.lo, c.d_ff, P, BN)))
+    return MOE_ERR_CUDA;
+  return launch_stream(L, mxfp4_layer_kernel<BN, kRoute>, p, kMxThreads, MxCfg<BN>::SMEM, kRoute,
+                       st);
+}
+
+template <int NT>
+moe_status launch_bf16_few(const moe_layer *L, const void *x, int T, void *out, void *ws,
+                           const WsLayout &W, cudaStream_t st) {
+  StreamParams p;
+  memset(&p, 0, sizeof p);
+  p.b = stream_base(L, x, T, out, ws, W);
+  p.tm_g = L->tm_st_g;
+  p.tm_u = L->tm_st_u;
+  p.tm_d = L->tm_st_d;
+  p.h = at<__nv_bfloat16>(ws, W.h);
+  return launch_stream(L, weight_stream_kernel<NT>, p, kStreamThreads, StreamCfg<NT>::SMEM, true,
+                       st);
+}
+
+// The whole layer in one launch (few_shape).
 moe_status forward_few(const moe_layer *L, const void *x, int T, void *out, void *ws,
                        cudaStream_t st) {
-  const StreamParams p = stream_params(L, x, T, out, ws, ws_layout(L->cfg, T, L->mx != 0));
-  if (L->mx)
-    return T <= 8 ? launch_stream<true, 1, true>(L, p, st) : launch_stream<true, 2, true>(L, p, st);
-  return T <= 8 ? launch_stream<false, 1, true>(L, p, st) : launch_stream<false, 2, true>(L, p, st);
+  const WsLayout W = ws_layout(L->cfg, T, L->mx != 0);
+  if (!L->mx)
+    return T <= 8 ? launch_bf16_few<1>(L, x, T, out, ws, W, st)
+                  : launch_bf16_few<2>(L, x, T, out, ws, W, st);
+  if (T <= 8) return launch_mx<8, true>(L, x, T, out, ws, W, st);
+  return T <= 16 ? launch_mx<16, true>(L, x, T, out, ws, W, st)
+                 : launch_mx<32, true>(L, x, T, out, ws, W, st);
 }
 
 // moe_forward of an MXFP4 handle.
 moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, void *ws,
                          cudaStream_t st) {
-  if (few_ok(L, T)) return forward_few(L, x, T, out, ws, st);
+  if (few_shape(L->cfg, T)) return forward_few(L, x, T, out, ws, st);
   const moe_config &c = L->cfg;
   const WsLayout W = ws_layout(c, T, true);
   DevStatus *status = at<DevStatus>(ws, W.status);
   const CounterReset reset{status->sched, at<int>(ws, W.done),
-                           c.n_experts + c.n_shared + c.d_model / kStreamMinTile};
+                           c.n_experts + c.n_shared + 1 + c.d_model / kStreamMinTile};
   float *logits = at<float>(ws, W.logits);
+  const size_t P = (size_t)T * (c.top_k + c.n_shared);
   moe_status s;
   if ((s = launch_logits(L, x, T, logits, at<float>(ws, W.part), status, st)) != MOE_OK ||
       (s = launch_select_permute(L, logits, T, nullptr, at<int>(ws, W.idx),
@@ -1489,17 +1567,21 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
                                  at<int>(ws, W.offsets), at<int>(ws, W.perm),
                                  at<int>(ws, W.slot_row), at<int>(ws, W.chunk_hist), reset,
                                  st)) != MOE_OK ||
-      (s = launch(act_block_scale_kernel,
+      (s = launch(split_rows_kernel,
                   dim3(grid_for((size_t)T * c.d_model / kMxPerLane, 256, L->num_sms)), dim3(256),
-                  0, st, static_cast<const __nv_bfloat16 *>(x), T, c.d_model,
-                  at<uint8_t>(ws, W.xq))) != MOE_OK)
+                  0, st, static_cast<const __nv_bfloat16 *>(x), at<int>(ws, W.slot_row), T,
+                  c.d_model, c.top_k, c.n_shared,
+                  split_rows(at<uint8_t>(ws, W.x_split), at<uint8_t>(ws, W.x_scale), P,
+                             c.d_model))) != MOE_OK)
     return s;
-  return launch_stream<true, 2, false>(L, stream_params(L, x, T, out, ws, W), st);
+  return (long long)T * c.top_k <= 16ll * c.n_experts
+             ? launch_mx<32, false>(L, x, T, out, ws, W, st)
+             : launch_mx<56, false>(L, x, T, out, ws, W, st);
 }
 
 int mxfp4_launches(const moe_layer *L, int T) {
   if (T == 0) return 0;
-  if (few_ok(L, T)) return 1;
+  if (few_shape(L->cfg, T)) return 1;
   return (T <= kChunk ? 2 : 3) + 2;
 }
 }  // namespace
@@ -1650,7 +1732,7 @@ moe_status moe_forward_few(moe_handle h, const void *x, int n_tokens, void *out,
   if (s != MOE_OK) return s;
   if (!holds_all_experts(h)) return MOE_ERR_UNSUPPORTED;  // an expert-parallel slice
   if (n_tokens == 0) return MOE_OK;
-  if (!few_ok(h, n_tokens)) return MOE_ERR_UNSUPPORTED;
+  if (!few_shape(h->cfg, n_tokens)) return MOE_ERR_UNSUPPORTED;
   if (!x || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(out)) return MOE_ERR_ALIGNMENT;
   return forward_few(h, x, n_tokens, out, ws, static_cast<cudaStream_t>(stream));
@@ -1698,6 +1780,18 @@ moe_status moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, lon
                   codes, scales, lanes, static_cast<__nv_bfloat16 *>(dst));
   return launch(mxfp4_dequantize_kernel<float>, mxfp4_grid(lanes), dim3(256), 0, st, codes,
                 scales, lanes, static_cast<float *>(dst));
+}
+
+moe_status moe_mxfp4_tile_scales(const uint8_t *scales, long long rows, int cols, uint8_t *tiled,
+                                 void *stream) {
+  if (rows < 0 || rows % kMxTile != 0 || cols < 0 || cols % 128 != 0) return MOE_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!scales || !tiled || rows > (1ll << 62) / cols) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(scales) || !aligned16(tiled)) return MOE_ERR_ALIGNMENT;
+  const size_t words = (size_t)rows * (cols / 128);
+  return launch(mxfp4_tile_scales_kernel, mxfp4_grid(words), dim3(256), 0,
+                static_cast<cudaStream_t>(stream), reinterpret_cast<const uint32_t *>(scales), words,
+                cols / 128, reinterpret_cast<uint32_t *>(tiled));
 }
 
 moe_status moe_forward_profiled(moe_handle h, const void *x, int n_tokens, void *out,

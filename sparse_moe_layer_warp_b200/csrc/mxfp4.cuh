@@ -1,5 +1,5 @@
-// mxfp4.cuh -- MXFP4 matrices (microscaled 4-bit floating point): quantisation, its inverse,
-// and the block-scaled fp16 activations that the weight-streaming kernels multiply them with.
+// mxfp4.cuh -- MXFP4 matrices (microscaled 4-bit floating point): quantisation, its inverse, and the
+// order of the scales that the layer's kernels load.
 //
 // A matrix [rows, cols] (cols a multiple of 32) is held as codes [rows, cols / 2] (two e2m1
 // values a byte, the lower column in the low nibble) and scales [rows, cols / 32] (one e8m0 byte
@@ -24,14 +24,18 @@ __device__ __forceinline__ float e8m0_to_f32(uint32_t byte) {
   return __uint_as_float(byte == 0 ? 0x00400000u : (byte == 255u ? 0x7fffffffu : byte << 23));
 }
 
-// eight e2m1 codes (low nibble first) -> eight halves, exact
+// Eight e2m1 codes (low nibble first) -> eight halves, exact: one conversion for each byte.  The
+// byte registers matter: through the header's 8-bit function, which packs and unpacks each result,
+// the same conversions ran at 28 codes a clock and SM instead of 124.
 __device__ __forceinline__ void e2m1x8_to_half(uint32_t codes, uint32_t (&h)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2_raw r = __nv_cvt_fp4x2_to_halfraw2(
-        static_cast<__nv_fp4x2_storage_t>((codes >> (8 * i)) & 0xffu), __NV_E2M1);
-    h[i] = (uint32_t)r.x | ((uint32_t)r.y << 16);
-  }
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(codes));
 }
 
 __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
@@ -131,6 +135,21 @@ __global__ void __launch_bounds__(256)
       v[2 * j + 1] = f.y * s;
     }
     store8(dst + i * kMxPerLane, v);
+  }
+}
+
+// Scales in the order of the block-scaled tensor core instruction: blocks of 512 bytes for 128 rows
+// x 128 K (a row of blocks after the other), in a block byte r % 32 * 16 + r / 32 * 4 + k / 32.
+// One thread moves the four scales of a row of a block (one word); n words, nk blocks along K.
+__global__ void __launch_bounds__(256)
+    mxfp4_tile_scales_kernel(const uint32_t *__restrict__ scales, size_t n, int nk,
+                             uint32_t *__restrict__ tiled) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const size_t step = (size_t)gridDim.x * blockDim.x;
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
+    const size_t block = i >> 7, row = block / nk * 128 + (i & 3) * 32 + ((i >> 2) & 31);
+    tiled[i] = scales[row * nk + block % nk];
   }
 }
 

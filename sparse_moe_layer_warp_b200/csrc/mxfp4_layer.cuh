@@ -1,0 +1,608 @@
+// mxfp4_layer.cuh -- the experts (and, for a few tokens, the whole layer) over MXFP4 weights in one
+// persistent kernel on the block-scaled tensor cores.
+//
+// Arithmetic.  The weights' e2m1 codes and e8m0 scales go to tcgen05.mma (.kind::mxf8f6f4,
+// .block_scale) as they are: no unpacking by the CUDA cores.  The other operand of that
+// instruction has at most 8 bits, so an activation is the sum of two e4m3 values, hi = round(v) and
+// lo = round(v - hi), each with one power-of-two scale for 32 neighbours (the largest of a block
+// lies in [2^7, 2^8) of hi's scale; lo's scale is 2^-4 of hi's).  e4m3 keeps four bits, so hi + lo
+// is a bf16 value exactly down to 2^-13 of its block's largest, and within 2^-21 of that largest
+// below; h (fp32 from the SwiGLU) is held to 2^-9 of itself, as by a rounding to bf16.  hi and lo
+// are separate columns of the N side; the epilogue adds the two fp32 accumulators.  N = 2 x tokens
+// at twice the bf16 rate: the tensor time of bf16, at 17/64 of its weight bytes.
+//
+// A stage: 128 K of two tiles of 128 weight rows (gate and up; two neighbouring tiles of W_d), in
+// shared memory one byte a code (the padded 4-bit TMA format: 8 bytes of codes, 8 of padding,
+// whose transaction count is the bytes read), their scales, and the 2 x BN token rows with theirs.
+// Scales are copied to TMEM by tcgen05.cp in the order of the instruction's scale layout: blocks of
+// 512 bytes for 128 rows x 128 K, byte (r % 32) * 16 + r / 32 * 4 + k / 32.
+//
+// Bound by HBM while a group has a few tokens (a stage is 17 KB of weights), by the tensor cores
+// and the delivery of their operands after that.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <stdint.h>
+
+#include "mxfp4.cuh"
+#include "stream_common.cuh"
+
+namespace moe {
+
+constexpr int kMxWarps = 16;  // 0-3 epilogue, 4 MMA, 5-6 weights, 7 token rows, 8 scheduler; the
+                              // others route (one-launch layer) and combine
+constexpr int kMxThreads = 32 * kMxWarps;
+constexpr int kMxTile = 128;  // weight rows of a tile: h columns of an up unit
+constexpr int kMxDown = 2 * kMxTile;  // y columns of a down unit
+constexpr int kMxScaleBlock = 512;
+
+// bytes of a row of activation scales: whole cache lines, so a line of h's scales never holds rows
+// that are still to be written beside rows that are read
+__host__ __device__ constexpr int act_scale_ld(int cols) { return (cols / 32 + 127) / 128 * 128; }
+
+// Activations as hi and lo e4m3 values [rows, cols] with their scale bytes [rows, act_scale_ld].
+struct SplitRows {
+  uint8_t *hi, *lo, *s_hi, *s_lo;
+};
+__host__ __forceinline__ SplitRows split_rows(uint8_t *values, uint8_t *scales, size_t rows,
+                                              int cols) {
+  return {values, values + rows * cols, scales, scales + rows * act_scale_ld(cols)};
+}
+
+struct MxParams {
+  StreamBase b;
+  CUtensorMap tm_g, tm_u, tm_d;              // codes, box {128, 128}, padded 4-bit
+  CUtensorMap tm_xhi, tm_xlo, tm_hhi, tm_hlo;  // token rows by TMA: box {128, BN}
+  const uint8_t *sc_g, *sc_u, *sc_d;         // scale blocks (mxfp4_tile_scales_kernel)
+  SplitRows x, h;                            // x: rows by token, or (TMA) by sorted row
+};
+
+template <int BN>
+struct MxCfg {
+  static constexpr int N = 2 * BN;                 // MMA N: hi rows, lo rows
+  static constexpr int A_BYTES = 2 * kMxTile * 128;
+  static constexpr int B_BYTES = N * 128;
+  static constexpr int SA_BYTES = 2 * kMxScaleBlock, SB_BYTES = kMxScaleBlock;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
+  static constexpr int ACC_COLS = 2 * N;           // both weight tiles
+  static constexpr int SF_COLS = 16;               // scale columns of a stage; two sets in turn
+  static constexpr int TMEM_USED = 2 * ACC_COLS + 2 * SF_COLS;
+  static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : (TMEM_USED <= 256 ? 256 : 512);
+  static_assert(TMEM_USED <= 512 && N % 16 == 0 && N <= 128 && B_BYTES % 1024 == 0, "tile");
+  static constexpr int FIXED = StreamTables::BYTES + 1024 /*barriers*/ + 1024 /*alignment*/;
+  static constexpr int STAGES_RAW = (226 * 1024 - FIXED) / STAGE_BYTES;
+  static constexpr int STAGES = STAGES_RAW > 8 ? 8 : STAGES_RAW;
+  static_assert(STAGES >= 3, "pipeline too shallow");
+  static_assert(STAGES * STAGE_BYTES >= kRouteScratch, "the ring holds the routing's scratch");
+  static constexpr size_t SMEM = FIXED + (size_t)STAGES * STAGE_BYTES;
+};
+
+// Untiled copy of `bytes` (a multiple of 16) from global into shared memory.
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Instruction descriptor, .kind::mxf8f6f4: A e2m1 (5 at bits 7-9), B e4m3 (0 at 10-12), both
+// K-major, N >> 3 at bits 17-22, e8m0 scales (bit 23), M >> 4 at bits 24-28; the byte of the scale
+// words that a step uses (K block 0..3) at bits 4-5 (B) and 29-30 (A).
+__device__ __forceinline__ constexpr uint32_t idesc_mx(int M, int N) {
+  return (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t sf_a, uint32_t sf_b, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sf_a), "r"(sf_b)
+      : "memory");
+}
+// One 512-byte scale block -> 4 TMEM columns of all four lane quadrants (rows of 16 bytes, groups
+// of 8 rows 128 bytes apart, no swizzle).  Runs in order with the thread's MMAs.
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(128u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
+// Scale byte of hi for a block whose largest magnitude has these fp32 bits: the largest lies in
+// [2^7, 2^8) of 2^(byte - 127).  lo's byte is 4 less (not below 0).
+__device__ __forceinline__ uint32_t act_scale_byte(uint32_t amax_bits) {
+  const uint32_t e = min(amax_bits >> 23, 254u);
+  return e > 7u ? e - 7u : 0u;
+}
+// Two values of (up to) two blocks -> hi and lo byte pairs; s: the blocks' scale bytes.
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t sa, uint32_t sb, uint32_t &hi,
+                                           uint32_t &lo) {
+  // an infinity becomes NaN: e4m3 has none, and a finite stand-in would be a wrong answer
+  a = fmaf(a, 0.f, a);
+  b = fmaf(b, 0.f, b);
+  a *= __uint_as_float((254u - sa) << 23);
+  b *= __uint_as_float((254u - sb) << 23);
+  uint16_t h, l;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(b), "f"(a));
+  uint32_t back;  // the pair as halves, exact
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(h));
+  const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&back));
+  // lo's unit: 2^-4 of hi's, or the smallest scale there is
+  const float ua = sa >= 4u ? 16.f : __uint_as_float((127u + sa) << 23);
+  const float ub = sb >= 4u ? 16.f : __uint_as_float((127u + sb) << 23);
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"((b - r.y) * ub), "f"((a - r.x) * ua));
+  hi = h;
+  lo = l;
+}
+__device__ __forceinline__ uint32_t lo_scale_byte(uint32_t s) { return s > 4u ? s - 4u : 0u; }
+
+// Eight neighbours a lane, four lanes a block, to rows of `out` (row r at r * d).
+__device__ __forceinline__ void split_lane(const float (&v)[8], uint2 &hi, uint2 &lo,
+                                           uint32_t &s) {
+  s = act_scale_byte(block_amax_bits(v));
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) split_pair(v[2 * j], v[2 * j + 1], s, s, h[j], l[j]);
+  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+__device__ __forceinline__ void store_split(const SplitRows &out, size_t row, int c, int cols,
+                                            const uint2 &hi, const uint2 &lo, uint32_t s) {
+  *reinterpret_cast<uint2 *>(out.hi + row * cols + c) = hi;
+  *reinterpret_cast<uint2 *>(out.lo + row * cols + c) = lo;
+  if ((c & 31) == 0) {
+    const size_t at = row * act_scale_ld(cols) + (c >> 5);
+    out.s_hi[at] = (uint8_t)s;
+    out.s_lo[at] = (uint8_t)lo_scale_byte(s);
+  }
+}
+
+// x [T, d] -> the split rows of the sorted space: token t to its k routed rows and its shared row.
+// One lane converts 8 neighbours and stores them k + n_shared times; bound by HBM (2 d bytes read,
+// 2 d (k + n_shared) written a token).
+__global__ void __launch_bounds__(256)
+    split_rows_kernel(const __nv_bfloat16 *__restrict__ x, const int *__restrict__ slot_row, int T,
+                      int d, int k, int n_shared, SplitRows out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lanes = d / kMxPerLane;  // a multiple of 16
+  const size_t n = (size_t)T * lanes, step = (size_t)gridDim.x * blockDim.x;
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < ((n + 31) & ~(size_t)31);
+       i += step) {
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (i < n) load8(x + i * kMxPerLane, v);
+    uint2 hi, lo;
+    uint32_t s;
+    split_lane(v, hi, lo, s);
+    if (i >= n) continue;
+    const int t = (int)(i / lanes), c = (int)(i % lanes) * kMxPerLane;
+    for (int j = 0; j < k; ++j)
+      store_split(out, __ldg(slot_row + (size_t)t * k + j), c, d, hi, lo, s);
+    if (n_shared) store_split(out, (size_t)T * k + t, c, d, hi, lo, s);
+  }
+}
+
+template <int BN, bool kRoute>
+__global__ void __launch_bounds__(kMxThreads, 1)
+    mxfp4_layer_kernel(const __grid_constant__ MxParams p) {
+  using C = MxCfg<BN>;
+  constexpr int S = C::STAGES, N = C::N;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *sA = smem;                       // [S][2 tiles][128 rows][128 B]
+  uint8_t *sB = sA + S * C::A_BYTES;        // [S][hi rows, lo rows][128 B]
+  uint8_t *sSA = sB + S * C::B_BYTES;       // [S][2][512]
+  uint8_t *sSB = sSA + S * C::SA_BYTES;     // [S][512]
+  uint64_t *full = reinterpret_cast<uint64_t *>(sSB + S * C::SB_BYTES);
+  uint64_t *empty = full + S;
+  uint64_t *tfull = empty + S;              // [2]
+  uint64_t *tempty = tfull + 2;             // [2]
+  uint64_t *uq_full = tempty + 2;
+  uint64_t *uq_empty = uq_full + kUnitQ;
+  uint64_t *mma_end = uq_empty + kUnitQ;    // all MMAs have completed
+  Unit *uq = reinterpret_cast<Unit *>(mma_end + 1);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(uq + kUnitQ);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  StreamTables tb(reinterpret_cast<uint8_t *>(full) + 1024, p.b.E, p.b.n_shared);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.b.E + p.b.n_shared, Tk = p.b.T * p.b.k, d = p.b.d, f = p.b.f;
+  const int up_tiles = f / kMxTile, down_tiles = (d + kMxDown - 1) / kMxDown;
+  const int n_rows = Tk + p.b.n_shared * p.b.T;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      // weights (two warps), token rows; by TMA: the rows' announcement and their scales'
+      mbar_init(&full[s], kRoute ? 3 : 4);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 4);
+    }
+    for (int q = 0; q < kUnitQ; ++q) {
+      mbar_init(&uq_full[q], 1);
+      mbar_init(&uq_empty[q], 8);  // epilogue 4, MMA, weights 2, token rows
+    }
+    mbar_init(mma_end, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_g);
+    tma_prefetch_desc(&p.tm_u);
+    tma_prefetch_desc(&p.tm_d);
+  }
+  if (warp == 4) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  const int *perm = kRoute ? tb.perm : p.b.perm;
+  const int *slot_row = kRoute ? tb.slot : p.b.slot_row;
+  const float *gate = kRoute ? tb.gate : p.b.gate;
+  bool alive = true;
+  __syncthreads();  // the abort flag is clear
+  if (kRoute) {
+    // split x by token, then route; the ring's memory is the scratch
+    const int lanes = d / kMxPerLane;
+    const size_t n = (size_t)p.b.T * lanes;
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < ((n + 31) & ~(size_t)31);
+         i += (size_t)gridDim.x * blockDim.x) {
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (i < n) load8(p.b.x + i * kMxPerLane, v);
+      uint2 hi, lo;
+      uint32_t s;
+      split_lane(v, hi, lo, s);
+      if (i < n) store_split(p.x, i / lanes, (int)(i % lanes) * kMxPerLane, d, hi, lo, s);
+    }
+    alive = route_tokens(p.b, tb, G + 1 + down_tiles, smem, abort_flag);
+  } else {
+    griddep_wait();
+    griddep_launch_dependents();
+    for (int e = threadIdx.x; e <= p.b.E; e += blockDim.x) tb.offsets[e] = p.b.offsets[e];
+  }
+  __syncthreads();
+  if (warp == 0 && alive) build_tile_prefix(p.b, tb, BN);
+  // the ring was the routing's scratch: its generic accesses precede the asynchronous copies
+  if (kRoute) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  // every lane polls; all of them see the phase, or the warp gives up
+  auto warp_wait = [&](uint64_t *bar, uint32_t parity, int where) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait_suspend(bar, parity, abort_flag, p.b.status, where));
+  };
+  // the next unit of the queue (qi, qph: this role's cursor); false when a wait gave up
+  int qi = 0;
+  uint32_t qph = 0;
+  auto next_unit = [&](Unit &w, int where) -> bool {
+    if (!warp_wait(&uq_full[qi], qph, where)) return false;
+    w = uq[qi];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&uq_empty[qi]);
+    if (++qi == kUnitQ) {
+      qi = 0;
+      qph ^= 1;
+    }
+    return true;
+  };
+
+  if (!alive) {
+    // the grid barrier gave up: no unit is claimed
+  } else if (warp == 8) {
+    if (lane == 0)
+      schedule_units(p.b, tb, BN, up_tiles, down_tiles, uq, uq_full, uq_empty, abort_flag);
+    __syncwarp();
+  } else if (warp == 5 || warp == 6) {
+    // ---------------------------------------------------------------- weights
+    // One warp for each of a stage's two tiles: issuing a copy takes a thread about 70 ns, waiting
+    // for the slot and announcing the bytes 150 ns more.
+    const int half = warp - 5;
+    const uint64_t pol_once = policy_evict_first(), pol_reuse = policy_evict_last();
+    int st = 0, filled = 0;
+    uint32_t ph = 0;
+    Unit w;
+    bool ok = true;
+    while ((ok = next_unit(w, 45)) && w.kind >= 0) {
+      if (lane == 0) {
+        const bool up = w.kind == 0;
+        const int nk = (up ? d : f) / 128, m_rows = up ? f : d;
+        const int tile = up ? w.mt : 2 * w.mt + half;
+        const bool there = tile * kMxTile < m_rows;  // d may be an odd number of tiles
+        const int row = w.g * m_rows + tile * kMxTile;
+        const CUtensorMap *m = up ? (half ? &p.tm_u : &p.tm_g) : &p.tm_d;
+        const uint8_t *sc = (up ? (half ? p.sc_u : p.sc_g) : p.sc_d) +
+                            (size_t)(row / kMxTile) * nk * kMxScaleBlock;
+        const uint64_t pol = w.uses == 1 ? pol_once : pol_reuse;
+        for (int kc = 0; kc < nk; ++kc) {
+          ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 32);
+          if (!ok) break;
+          if (there) {
+            mbar_arrive_expect_tx(&full[st], kMxTile * 64 + kMxScaleBlock);
+            tma_load_2d_hint(sA + st * C::A_BYTES + half * (C::A_BYTES / 2), m, &full[st],
+                             kc * 128, row, pol);
+            bulk_load(sSA + st * C::SA_BYTES + half * kMxScaleBlock, sc + kc * kMxScaleBlock,
+                      kMxScaleBlock, &full[st]);
+          } else {
+            mbar_arrive(&full[st]);
+          }
+          ++filled;
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) drain_stages(full, filled, S);
+    __syncwarp();
+  } else if (warp == 7) {
+    // ---------------------------------------------------------------- token rows
+    // One-launch layer: rows are gathered by 16-byte asynchronous copies, 8 lanes a row, into the
+    // swizzled tile.  Otherwise the rows of a unit are neighbours (x was split into sorted rows):
+    // two TMA boxes.  The scale words come by 4-byte copies either way.  The copies of up to
+    // kAhead stages are in flight; one lane announces a stage when they have landed.  Nothing is
+    // held back while the warp waits: it announces everything first.
+    constexpr int kAhead = 3;
+    const int h_target = n_rows * up_tiles * 4;
+    bool all_ready = false;
+    int st = 0, pending = 0, filled = 0;
+    uint32_t ph = 0;
+    Unit w;
+    bool ok = true;
+    auto announce = [&](int n) {  // the n oldest pending stages, whose copies have landed
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads them
+      __syncwarp();
+      if (lane == 0)
+        for (int i = 0; i < n; ++i) {
+          const int s = st - pending + i;
+          mbar_arrive(&full[s < 0 ? s + S : s]);
+        }
+      pending -= n;
+    };
+    auto flush = [&]() {
+      if (pending == 0) return;
+      cp_async_wait<0>();
+      announce(pending);
+    };
+    while (true) {
+      if (!__all_sync(0xffffffffu, mbar_try_wait(&uq_full[qi], qph))) flush();
+      ok = next_unit(w, 33);
+      if (!ok || w.kind < 0) break;
+      const bool up = w.kind == 0;
+      if (!up && !all_ready) {
+        flush();
+        // lane 0 waits for the group's h; lane 1 looks whether all of h is there, after which
+        // no unit asks again (each look costs an L2 round trip)
+        int got = 1;
+        if (lane == 0)
+          got = counter_wait_bounded(p.b.done + w.g, w.rows * up_tiles * 4, abort_flag,
+                                     p.b.status, 34);
+        if (lane == 1) got = counter_load(p.b.done_all) == h_target ? 2 : 1;
+        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+        if (!ok) break;
+        all_ready = __shfl_sync(0xffffffffu, got, 1) == 2;
+        __syncwarp();  // the other lanes' copies follow those two loads
+        if (!kRoute) fence_proxy_async_global();  // other CTAs' stores, read by TMA
+      }
+      const SplitRows &src = up ? p.x : p.h;
+      const int K = up ? d : f, nk = K / 128, ld = act_scale_ld(K);
+      // row of token i of the unit: one-launch x rows are by token
+      int my_row = w.row0 + lane;
+      if (kRoute && up && lane < w.n)
+        my_row = w.g < p.b.E ? perm[w.row0 + lane] / p.b.k : w.tok0 + lane;
+      for (int kc = 0; kc < nk; ++kc) {
+        if (!__all_sync(0xffffffffu, mbar_try_wait(&empty[st], ph ^ 1))) {
+          flush();
+          ok = warp_wait(&empty[st], ph ^ 1, 35);
+          if (!ok) break;
+        }
+        const uint32_t b = smem_u32(sB) + st * C::B_BYTES, sb = smem_u32(sSB) + st * C::SB_BYTES;
+        if (kRoute) {
+          const int c = lane & 7;  // 16-byte chunk of a 128-byte row
+          for (int r0 = 0; r0 < 2 * w.n; r0 += 4) {
+            const int r = r0 + (lane >> 3), i = r < w.n ? r : r - w.n;
+            const size_t row = __shfl_sync(0xffffffffu, my_row, i & 31);
+            const int to = r < w.n ? r : BN + i;  // row of the tile
+            if (r < 2 * w.n)
+              cp_async16(b + to * 128 + ((c ^ (to & 7)) << 4),
+                         (r < w.n ? src.hi : src.lo) + row * K + kc * 128 + c * 16);
+          }
+        } else if (lane == 0) {
+          mbar_arrive_expect_tx(&full[st], C::B_BYTES);
+          tma_load_2d(sB + st * C::B_BYTES, up ? &p.tm_xhi : &p.tm_hhi, &full[st], kc * 128,
+                      w.row0);
+          tma_load_2d(sB + st * C::B_BYTES + C::B_BYTES / 2, up ? &p.tm_xlo : &p.tm_hlo,
+                      &full[st], kc * 128, w.row0);
+        }
+        for (int r0 = 0; r0 < 2 * w.n; r0 += 32) {
+          const int r = r0 + lane, i = r < w.n ? r : r - w.n;
+          const size_t row = kRoute ? __shfl_sync(0xffffffffu, my_row, i & 31) : w.row0 + i;
+          const int to = r < w.n ? r : BN + i;
+          if (r < 2 * w.n)
+            cp_async4(sb + (to & 31) * 16 + (to >> 5) * 4,
+                      (r < w.n ? src.s_hi : src.s_lo) + row * ld + kc * 4);
+        }
+        cp_async_commit();
+        ++pending;
+        ++filled;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
+        }
+        if (pending == kAhead) {
+          cp_async_wait<kAhead - 1>();
+          announce(1);
+        }
+      }
+      if (!ok) break;
+    }
+    flush();
+    if (!ok && !kRoute && lane == 0) drain_stages(full, filled, S);
+    __syncwarp();
+  } else if (warp == 4) {
+    // ---------------------------------------------------------------- MMA
+    int st = 0, it = 0;
+    uint32_t ph = 0;
+    Unit w;
+    bool ok = true;
+    while ((ok = next_unit(w, 36)) && w.kind >= 0) {
+      const int acc = it & 1, nk = (w.kind == 0 ? d : f) / 128;
+      const bool two = w.kind == 0 || (2 * w.mt + 1) * kMxTile < d;
+      if (lane == 0) {
+        ok = mbar_wait_suspend(&tempty[acc], ((it >> 1) & 1) ^ 1, abort_flag, p.b.status, 46);
+        tc_fence_after();
+        const uint32_t d0 = tmem_base + acc * C::ACC_COLS;
+        for (int kc = 0; ok && kc < nk; ++kc) {
+          ok = mbar_wait_suspend(&full[st], ph, abort_flag, p.b.status, 37);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sf = tmem_base + 2 * C::ACC_COLS + (kc & 1) * C::SF_COLS;
+          const uint32_t sa = smem_u32(sSA) + st * C::SA_BYTES;
+          tc_cp_scales(sf, sa);
+          if (two) tc_cp_scales(sf + 4, sa + kMxScaleBlock);
+          tc_cp_scales(sf + 8, smem_u32(sSB) + st * C::SB_BYTES);
+          const uint32_t a = smem_u32(sA) + st * C::A_BYTES, b = smem_u32(sB) + st * C::B_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t id = idesc_mx(kMxTile, N) | ((uint32_t)kk << 4) | ((uint32_t)kk << 29);
+            const uint64_t bd = sdesc_k_sw128(b + kk * 32);
+            const uint32_t add = (kc | kk) ? 1u : 0u;
+            tc_mma_mx(d0, sdesc_k_sw128(a + kk * 32), bd, id, sf, sf + 8, add);
+            if (two)
+              tc_mma_mx(d0 + N, sdesc_k_sw128(a + C::A_BYTES / 2 + kk * 32), bd, id, sf + 4,
+                        sf + 8, add);
+          }
+          tc_commit(&empty[st]);
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) tc_commit(&tfull[acc]);
+      }
+      ++it;
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+    }
+    if (lane == 0) {
+      tc_commit(mma_end);
+      volatile int no_abort = 0;
+      mbar_wait_bounded(mma_end, 0, &no_abort, nullptr, 0);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---------------------------------------------------------------- epilogue
+    int it = 0;
+    Unit w;
+    while ((alive = next_unit(w, 42)) && w.kind >= 0) {
+      const int acc = it & 1;
+      const bool up = w.kind == 0;
+      const bool two = up || (2 * w.mt + 1) * kMxTile < d;
+      // down: routed_scale * gate of tokens lane and 32 + lane, asked for before the wait
+      float sc0 = 1.f, sc1 = 1.f;
+      if (!up && w.g < p.b.E) {
+        if (lane < w.n) sc0 = p.b.routed_scale * gate[perm[w.row0 + lane]];
+        if (BN > 32 && 32 + lane < w.n) sc1 = p.b.routed_scale * gate[perm[w.row0 + 32 + lane]];
+      }
+      alive = warp_wait(&tfull[acc], (it >> 1) & 1, 39);
+      if (!alive) break;
+      ++it;
+      tc_fence_after();
+      const uint32_t ta = tmem_base + ((uint32_t)(warp * 32) << 16) + acc * C::ACC_COLS;
+      for (int c = 0; c < w.n; c += 8) {
+        uint32_t r0[8], r1[8], r2[8], r3[8];
+        tmem_ld8(ta + c, r0);
+        tmem_ld8(ta + BN + c, r1);
+        if (two) {
+          tmem_ld8(ta + N + c, r2);
+          tmem_ld8(ta + N + BN + c, r3);
+        }
+        tmem_ld_wait();
+        float v0[8], v1[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v0[j] = __uint_as_float(r0[j]) + __uint_as_float(r1[j]);
+          v1[j] = two ? __uint_as_float(r2[j]) + __uint_as_float(r3[j]) : 0.f;
+        }
+        if (up) {
+          const int col = w.mt * kMxTile + warp * 32;  // a block of 32 columns of h
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            if (c + j >= w.n) break;
+            const float ha = swiglu(v0[j], v1[j]), hb = swiglu(v0[j + 1], v1[j + 1]);
+            const uint32_t sa = act_scale_byte(
+                __reduce_max_sync(0xffffffffu, __float_as_uint(ha) & 0x7fffffffu));
+            const uint32_t sb = act_scale_byte(
+                __reduce_max_sync(0xffffffffu, __float_as_uint(hb) & 0x7fffffffu));
+            uint32_t hi, lo;
+            split_pair(ha, hb, sa, sb, hi, lo);
+            const size_t row = w.row0 + c + j, at = row * f + col + lane;
+            p.h.hi[at] = (uint8_t)hi;
+            p.h.lo[at] = (uint8_t)lo;
+            const bool both = c + j + 1 < w.n;
+            if (both) {
+              p.h.hi[at + f] = (uint8_t)(hi >> 8);
+              p.h.lo[at + f] = (uint8_t)(lo >> 8);
+            }
+            if (lane < 4 && (both || lane < 2)) {  // lanes 0, 1: first token; 2, 3: second
+              const uint32_t s = lane < 2 ? sa : sb;
+              (lane & 1 ? p.h.s_lo : p.h.s_hi)[(row + (lane >> 1)) * act_scale_ld(f) + (col >> 5)] =
+                  (uint8_t)(lane & 1 ? lo_scale_byte(s) : s);
+            }
+          }
+        } else {
+          float *y = p.b.y + (size_t)(w.row0 + c) * d + w.mt * kMxDown + warp * 32 + lane;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float s = __shfl_sync(0xffffffffu, BN > 32 && c >= 32 ? sc1 : sc0, (c + j) & 31);
+            if (c + j < w.n) {
+              y[(size_t)j * d] = v0[j] * s;
+              if (two) y[(size_t)j * d + kMxTile] = v1[j] * s;
+            }
+          }
+        }
+      }
+      // every TMEM load has completed: the accumulator goes back before the stores drain
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&tempty[acc]);
+        // publish: the warp's stores (made visible by this fence, after the warp's barrier), then
+        // the count of its pieces of rows
+        __threadfence();
+        atomicAdd(up ? p.b.done + w.g : p.b.tile_done + w.mt, w.n);
+        if (up) atomicAdd(p.b.done_all, w.n);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------------- idle until the combine
+    alive = warp_wait(mma_end, 0, 47);
+  }
+  if (alive && (warp < 4 || warp > 8))
+    combine_pieces(p.b, slot_row, kMxDown, n_rows * 4, warp < 4 ? warp : warp - 5, kMxWarps - 5,
+                   abort_flag);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+  if (kRoute && threadIdx.x == 0) leave_grid(p.b);
+}
+
+}  // namespace moe

@@ -206,6 +206,18 @@ __device__ __forceinline__ void tma_load_2d_hint(void *dst, const CUtensorMap *m
       : "memory");
 }
 
+// 3-D tiled load with an L2 eviction-priority hint.
+__device__ __forceinline__ void tma_load_3d_hint(void *dst, const CUtensorMap *map,
+                                                 uint64_t *bar, int c0, int c1, int c2,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
+      "l"(policy)
+      : "memory");
+}
+
 // Row gather: four rows r0..r3 of a 2-D map whose box is {box columns, 1 row}, columns
 // [c0, c0 + box columns) of each, written as four consecutive box rows at dst.  The 128-byte
 // swizzle of the map is a function of the shared-memory address, so rows written at

@@ -147,16 +147,17 @@ bool encode_codes(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows
          CUDA_SUCCESS;
 }
 
-// Row-major bytes [rows, cols] -> map with box {128 bytes, box_rows rows} and 128-byte swizzle.
-bool encode_u8_2d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows,
+// Split activations (SplitRows: bytes [2][rows, cols]) -> map with box {128 columns, box_rows rows,
+// hi and lo} and 128-byte swizzle.
+bool encode_split(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows,
                   uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols};
-  cuuint32_t box[2] = {128, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+  cuuint64_t dims[3] = {cols, rows, 2};
+  cuuint64_t strides[2] = {cols, rows * cols};
+  cuuint32_t box[3] = {128, box_rows, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
@@ -249,6 +250,12 @@ bool few_shape(const moe_config &c, int T) {
   return decode_route_ok(c, T) && T <= kStreamMaxT && T * c.top_k <= kStreamMaxPairs;
 }
 
+// Token rows of a tile of the MXFP4 layer.
+int mx_token_tile(const moe_config &c, int T) {
+  if (few_shape(c, T)) return T <= 8 ? 8 : (T <= 16 ? 16 : 32);
+  return (long long)T * c.top_k <= 16ll * c.n_experts ? 32 : 56;
+}
+
 // mx: an MXFP4 handle's layout (x and h as pairs of e4m3 values with their scales; x by token for
 // the one-launch layer, by sorted row otherwise)
 WsLayout ws_layout(const moe_config &c, int T, bool mx = false) {
@@ -284,8 +291,10 @@ WsLayout ws_layout(const moe_config &c, int T, bool mx = false) {
   L.health = take(2 * ((size_t)c.n_experts + c.n_shared) * kHealthSlices * 8);
   const size_t x_rows = !mx ? 0 : few_shape(c, T) ? (size_t)T : P;
   L.x_split = take(2 * x_rows * c.d_model);
-  L.x_scale = take(2 * x_rows * act_scale_ld(c.d_model));
-  L.h_scale = take(mx ? 2 * P * act_scale_ld(c.d_ff) : 0);
+  // scale blocks of every token tile (x of the one-launch layer: words by token)
+  const size_t tiles = !mx ? 0 : P / mx_token_tile(c, T) + c.n_experts + c.n_shared;
+  L.x_scale = take((few_shape(c, T) ? x_rows * 8 : tiles * kMxScaleBlock) * (c.d_model / 128));
+  L.h_scale = take(tiles * kMxScaleBlock * (c.d_ff / 128));
   L.total = off;
   return L;
 }
@@ -1512,12 +1521,12 @@ moe_status launch_mx(const moe_layer *L, const void *x, int T, void *out, void *
   p.sc_g = L->sc_gate;
   p.sc_u = L->sc_up;
   p.sc_d = L->sc_down;
-  p.x = split_rows(at<uint8_t>(ws, W.x_split), at<uint8_t>(ws, W.x_scale), x_rows, c.d_model);
-  p.h = split_rows(at<uint8_t>(ws, W.h), at<uint8_t>(ws, W.h_scale), P, c.d_ff);
-  if (!kRoute && (!encode_u8_2d(&p.tm_xhi, p.x.hi, c.d_model, P, BN) ||
-                  !encode_u8_2d(&p.tm_xlo, p.x.lo, c.d_model, P, BN) ||
-                  !encode_u8_2d(&p.tm_hhi, p.h.hi, c.d_ff, P, BN) ||
-                  !encode_u8_2d(&p.tm_hlo, p.h.lo, c.d_ff, P, BN)))
+  p.x = split_rows(at<uint8_t>(ws, W.x_split), x_rows, c.d_model);
+  p.h = split_rows(at<uint8_t>(ws, W.h), P, c.d_ff);
+  p.xs = at<uint8_t>(ws, W.x_scale);
+  p.hs = at<uint8_t>(ws, W.h_scale);
+  if ((!kRoute && !encode_split(&p.tm_x, p.x.hi, c.d_model, P, BN)) ||
+      !encode_split(&p.tm_h, p.h.hi, c.d_ff, P, BN))
     return MOE_ERR_CUDA;
   return launch_stream(L, mxfp4_layer_kernel<BN, kRoute>, p, kMxThreads, MxCfg<BN>::SMEM, kRoute,
                        st);
@@ -1544,9 +1553,11 @@ moe_status forward_few(const moe_layer *L, const void *x, int T, void *out, void
   if (!L->mx)
     return T <= 8 ? launch_bf16_few<1>(L, x, T, out, ws, W, st)
                   : launch_bf16_few<2>(L, x, T, out, ws, W, st);
-  if (T <= 8) return launch_mx<8, true>(L, x, T, out, ws, W, st);
-  return T <= 16 ? launch_mx<16, true>(L, x, T, out, ws, W, st)
-                 : launch_mx<32, true>(L, x, T, out, ws, W, st);
+  switch (mx_token_tile(L->cfg, T)) {
+    case 8: return launch_mx<8, true>(L, x, T, out, ws, W, st);
+    case 16: return launch_mx<16, true>(L, x, T, out, ws, W, st);
+  }
+  return launch_mx<32, true>(L, x, T, out, ws, W, st);
 }
 
 // moe_forward of an MXFP4 handle.
@@ -1568,15 +1579,15 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
                                  at<int>(ws, W.slot_row), at<int>(ws, W.chunk_hist), reset,
                                  st)) != MOE_OK ||
       (s = launch(split_rows_kernel,
-                  dim3(grid_for((size_t)T * c.d_model / kMxPerLane, 256, L->num_sms)), dim3(256),
-                  0, st, static_cast<const __nv_bfloat16 *>(x), at<int>(ws, W.slot_row), T,
-                  c.d_model, c.top_k, c.n_shared,
-                  split_rows(at<uint8_t>(ws, W.x_split), at<uint8_t>(ws, W.x_scale), P,
-                             c.d_model))) != MOE_OK)
+                  dim3(grid_for((size_t)T, 8, L->num_sms)), dim3(256), 0, st,
+                  static_cast<const __nv_bfloat16 *>(x), at<int>(ws, W.slot_row),
+                  at<int>(ws, W.idx), at<int>(ws, W.offsets), T, c.d_model, c.n_experts, c.top_k,
+                  c.n_shared, mx_token_tile(c, T),
+                  split_rows(at<uint8_t>(ws, W.x_split), P, c.d_model),
+                  at<uint8_t>(ws, W.x_scale))) != MOE_OK)
     return s;
-  return (long long)T * c.top_k <= 16ll * c.n_experts
-             ? launch_mx<32, false>(L, x, T, out, ws, W, st)
-             : launch_mx<56, false>(L, x, T, out, ws, W, st);
+  return mx_token_tile(c, T) == 32 ? launch_mx<32, false>(L, x, T, out, ws, W, st)
+                                   : launch_mx<56, false>(L, x, T, out, ws, W, st);
 }
 
 int mxfp4_launches(const moe_layer *L, int T) {

@@ -37,25 +37,26 @@ constexpr int kMxTile = 128;  // weight rows of a tile: h columns of an up unit
 constexpr int kMxDown = 2 * kMxTile;  // y columns of a down unit
 constexpr int kMxScaleBlock = 512;
 
-// bytes of a row of activation scales: whole cache lines, so a line of h's scales never holds rows
-// that are still to be written beside rows that are read
-__host__ __device__ constexpr int act_scale_ld(int cols) { return (cols / 32 + 127) / 128 * 128; }
-
-// Activations as hi and lo e4m3 values [rows, cols] with their scale bytes [rows, act_scale_ld].
+// Activations as hi and lo e4m3 values: hi [rows, cols], lo behind it.
 struct SplitRows {
-  uint8_t *hi, *lo, *s_hi, *s_lo;
+  uint8_t *hi, *lo;
 };
-__host__ __forceinline__ SplitRows split_rows(uint8_t *values, uint8_t *scales, size_t rows,
-                                              int cols) {
-  return {values, values + rows * cols, scales, scales + rows * act_scale_ld(cols)};
+__host__ __forceinline__ SplitRows split_rows(uint8_t *values, size_t rows, int cols) {
+  return {values, values + rows * cols};
 }
+
+// Their scales come in blocks as the weights' do, one for each token tile of BN rows and 128
+// columns (token_tile_number): rows 0 .. BN - 1 of a block are hi's, BN .. 2 BN - 1 lo's.
+__device__ __forceinline__ int scale_row_at(int r) { return (r & 31) * 16 + (r >> 5) * 4; }
 
 struct MxParams {
   StreamBase b;
   CUtensorMap tm_g, tm_u, tm_d;              // codes, box {128, 128}, padded 4-bit
-  CUtensorMap tm_xhi, tm_xlo, tm_hhi, tm_hlo;  // token rows by TMA: box {128, BN}
+  CUtensorMap tm_x, tm_h;                    // token rows: box {128, BN, hi and lo}
   const uint8_t *sc_g, *sc_u, *sc_d;         // scale blocks (mxfp4_tile_scales_kernel)
-  SplitRows x, h;                            // x: rows by token, or (TMA) by sorted row
+  SplitRows x, h;                            // x: rows by token (one-launch layer), or sorted
+  uint8_t *xs, *hs;                          // scale blocks by token tile and 128 columns; one-
+                                             // launch layer: xs words by token and 128 columns
 };
 
 template <int BN>
@@ -149,49 +150,81 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t sa, uint32
 }
 __device__ __forceinline__ uint32_t lo_scale_byte(uint32_t s) { return s > 4u ? s - 4u : 0u; }
 
-// Eight neighbours a lane, four lanes a block, to rows of `out` (row r at r * d).
-__device__ __forceinline__ void split_lane(const float (&v)[8], uint2 &hi, uint2 &lo,
-                                           uint32_t &s) {
-  s = act_scale_byte(block_amax_bits(v));
-  uint32_t h[4], l[4];
+// 16 neighbours a lane, two lanes a block, eight lanes a scale word: this lane's values as hi and lo
+// bytes, and the four scale bytes of the eight lanes (valid in every lane).
+__device__ __forceinline__ void split_lane(const float (&v)[16], uint4 &hi, uint4 &lo,
+                                           uint32_t &s_hi, uint32_t &s_lo) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) split_pair(v[2 * j], v[2 * j + 1], s, s, h[j], l[j]);
-  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  const uint32_t s = act_scale_byte(max(m, __shfl_xor_sync(0xffffffffu, m, 1)));
+  uint32_t h[8], l[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) split_pair(v[2 * j], v[2 * j + 1], s, s, h[j], l[j]);
+  hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  lo = make_uint4(l[0] | l[1] << 16, l[2] | l[3] << 16, l[4] | l[5] << 16, l[6] | l[7] << 16);
+  const int shift = (threadIdx.x & 6) * 4;  // block of this lane among the eight lanes' four
+  s_hi = s << shift;
+  s_lo = lo_scale_byte(s) << shift;
+#pragma unroll
+  for (int o = 2; o < 8; o <<= 1) {
+    s_hi |= __shfl_xor_sync(0xffffffffu, s_hi, o);
+    s_lo |= __shfl_xor_sync(0xffffffffu, s_lo, o);
+  }
 }
-__device__ __forceinline__ void store_split(const SplitRows &out, size_t row, int c, int cols,
-                                            const uint2 &hi, const uint2 &lo, uint32_t s) {
-  *reinterpret_cast<uint2 *>(out.hi + row * cols + c) = hi;
-  *reinterpret_cast<uint2 *>(out.lo + row * cols + c) = lo;
-  if ((c & 31) == 0) {
-    const size_t at = row * act_scale_ld(cols) + (c >> 5);
-    out.s_hi[at] = (uint8_t)s;
-    out.s_lo[at] = (uint8_t)lo_scale_byte(s);
+__device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[16]) {
+  float a[8], b[8];
+  load8(p, a);
+  load8(p + 8, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[i] = a[i];
+    v[8 + i] = b[i];
   }
 }
 
-// x [T, d] -> the split rows of the sorted space: token t to its k routed rows and its shared row.
-// One lane converts 8 neighbours and stores them k + n_shared times; bound by HBM (2 d bytes read,
-// 2 d (k + n_shared) written a token).
+// x [T, d] -> the split rows of the sorted space with their scale blocks: token t to its k routed
+// rows and its shared row.  One warp a token: converts 512 columns at a time and stores them
+// k + n_shared times; bound by HBM (2 d bytes read, 2 d (k + n_shared) written a token).
 __global__ void __launch_bounds__(256)
-    split_rows_kernel(const __nv_bfloat16 *__restrict__ x, const int *__restrict__ slot_row, int T,
-                      int d, int k, int n_shared, SplitRows out) {
+    split_rows_kernel(const __nv_bfloat16 *__restrict__ x, const int *__restrict__ slot_row,
+                      const int *__restrict__ idx, const int *__restrict__ offsets, int T, int d,
+                      int E, int k, int n_shared, int BN, SplitRows out, uint8_t *xs) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lanes = d / kMxPerLane;  // a multiple of 16
-  const size_t n = (size_t)T * lanes, step = (size_t)gridDim.x * blockDim.x;
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < ((n + 31) & ~(size_t)31);
-       i += step) {
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (i < n) load8(x + i * kMxPerLane, v);
-    uint2 hi, lo;
-    uint32_t s;
-    split_lane(v, hi, lo, s);
-    if (i >= n) continue;
-    const int t = (int)(i / lanes), c = (int)(i % lanes) * kMxPerLane;
-    for (int j = 0; j < k; ++j)
-      store_split(out, __ldg(slot_row + (size_t)t * k + j), c, d, hi, lo, s);
-    if (n_shared) store_split(out, (size_t)T * k + t, c, d, hi, lo, s);
+  const int lane = threadIdx.x & 31, nk = d / 128, n_warps = gridDim.x * 8;
+  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += n_warps) {
+    // lane j: row of slot j (the shared row last), its tile's scale blocks, its place in a block
+    int row = 0, tile = 0, r = 0;
+    if (lane < k + n_shared) {
+      const int g = lane < k ? idx[(size_t)t * k + lane] : E;
+      const int off = lane < k ? offsets[g] : T * k;
+      row = lane < k ? slot_row[(size_t)t * k + lane] : T * k + t;
+      tile = token_tile_number(off, g, (row - off) / BN, BN);
+      r = (row - off) % BN;
+    }
+    for (int c0 = 0; c0 < d; c0 += 512) {
+      const int c = c0 + lane * 16;
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.f;
+      if (c < d) load16(x + (size_t)t * d + c, v);
+      uint4 hi, lo;
+      uint32_t s_hi, s_lo;
+      split_lane(v, hi, lo, s_hi, s_lo);
+      for (int j = 0; j < k + n_shared; ++j) {
+        const size_t rw = __shfl_sync(0xffffffffu, row, j);
+        const size_t tl = __shfl_sync(0xffffffffu, tile, j);
+        const int rj = __shfl_sync(0xffffffffu, r, j);
+        if (c >= d) continue;
+        *reinterpret_cast<uint4 *>(out.hi + rw * d + c) = hi;
+        *reinterpret_cast<uint4 *>(out.lo + rw * d + c) = lo;
+        if ((lane & 7) < 2)
+          *reinterpret_cast<uint32_t *>(xs + (tl * nk + (c >> 7)) * kMxScaleBlock +
+                                        scale_row_at((lane & 1) ? BN + rj : rj)) =
+              (lane & 1) ? s_lo : s_hi;
+      }
+    }
   }
 }
 
@@ -226,8 +259,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      // weights (two warps), token rows; by TMA: the rows' announcement and their scales'
-      mbar_init(&full[s], kRoute ? 3 : 4);
+      mbar_init(&full[s], 3);  // weights (two warps), token rows
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -253,16 +285,22 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   __syncthreads();  // the abort flag is clear
   if (kRoute) {
     // split x by token, then route; the ring's memory is the scratch
-    const int lanes = d / kMxPerLane;
-    const size_t n = (size_t)p.b.T * lanes;
-    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < ((n + 31) & ~(size_t)31);
-         i += (size_t)gridDim.x * blockDim.x) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (i < n) load8(p.b.x + i * kMxPerLane, v);
-      uint2 hi, lo;
-      uint32_t s;
-      split_lane(v, hi, lo, s);
-      if (i < n) store_split(p.x, i / lanes, (int)(i % lanes) * kMxPerLane, d, hi, lo, s);
+    const int nk = d / 128, chunks = (d + 511) / 512, n_warps = gridDim.x * kMxWarps;
+    for (int i = blockIdx.x * kMxWarps + warp; i < p.b.T * chunks; i += n_warps) {
+      const int t = i / chunks, c = (i % chunks) * 512 + lane * 16;
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = 0.f;
+      if (c < d) load16(p.b.x + (size_t)t * d + c, v);
+      uint4 hi, lo;
+      uint32_t s_hi, s_lo;
+      split_lane(v, hi, lo, s_hi, s_lo);
+      if (c >= d) continue;
+      *reinterpret_cast<uint4 *>(p.x.hi + (size_t)t * d + c) = hi;
+      *reinterpret_cast<uint4 *>(p.x.lo + (size_t)t * d + c) = lo;
+      if ((lane & 7) == 0)
+        *reinterpret_cast<uint2 *>(p.xs + ((size_t)t * nk + (c >> 7)) * 8) =
+            make_uint2(s_hi, s_lo);
     }
     alive = route_tokens(p.b, tb, G + 1 + down_tiles, smem, abort_flag);
   } else {
@@ -351,11 +389,12 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     __syncwarp();
   } else if (warp == 7) {
     // ---------------------------------------------------------------- token rows
-    // One-launch layer: rows are gathered by 16-byte asynchronous copies, 8 lanes a row, into the
-    // swizzled tile.  Otherwise the rows of a unit are neighbours (x was split into sorted rows):
-    // two TMA boxes.  The scale words come by 4-byte copies either way.  The copies of up to
-    // kAhead stages are in flight; one lane announces a stage when they have landed.  Nothing is
-    // held back while the warp waits: it announces everything first.
+    // The rows of a unit are neighbours (x was split into sorted rows): a stage's come in one box,
+    // its scales in one block.  Only x of the one-launch layer is by token: its rows are gathered
+    // by 16-byte asynchronous copies, 8 lanes a row, into the swizzled tile, the scale words by
+    // 4-byte copies; the copies of up to kAhead stages are in flight, and one lane announces a
+    // stage when they have landed.  Nothing is held back while the warp waits: it announces
+    // everything first.
     constexpr int kAhead = 3;
     const int h_target = n_rows * up_tiles * 4;
     bool all_ready = false;
@@ -396,14 +435,37 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         if (!ok) break;
         all_ready = __shfl_sync(0xffffffffu, got, 1) == 2;
         __syncwarp();  // the other lanes' copies follow those two loads
-        if (!kRoute) fence_proxy_async_global();  // other CTAs' stores, read by TMA
+        fence_proxy_async_global();  // other CTAs' stores, read by TMA
       }
-      const SplitRows &src = up ? p.x : p.h;
-      const int K = up ? d : f, nk = K / 128, ld = act_scale_ld(K);
-      // row of token i of the unit: one-launch x rows are by token
+      const int K = up ? d : f, nk = K / 128;
+      if (!kRoute || !up) {
+        flush();
+        if (lane == 0) {
+          const CUtensorMap *m = up ? &p.tm_x : &p.tm_h;
+          const uint8_t *sc = (up ? p.xs : p.hs) + (size_t)w.tile * nk * kMxScaleBlock;
+          for (int kc = 0; kc < nk; ++kc) {
+            ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 35);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&full[st], C::B_BYTES + kMxScaleBlock);
+            tma_load_3d(sB + st * C::B_BYTES, m, &full[st], kc * 128, w.row0, 0);
+            bulk_load(sSB + st * C::SB_BYTES, sc + kc * kMxScaleBlock, kMxScaleBlock, &full[st]);
+            ++filled;
+            if (++st == S) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+        }
+        st = __shfl_sync(0xffffffffu, st, 0);
+        ph = __shfl_sync(0xffffffffu, ph, 0);
+        filled = __shfl_sync(0xffffffffu, filled, 0);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        continue;
+      }
+      // row of token i of the unit
       int my_row = w.row0 + lane;
-      if (kRoute && up && lane < w.n)
-        my_row = w.g < p.b.E ? perm[w.row0 + lane] / p.b.k : w.tok0 + lane;
+      if (lane < w.n) my_row = w.g < p.b.E ? perm[w.row0 + lane] / p.b.k : w.tok0 + lane;
       for (int kc = 0; kc < nk; ++kc) {
         if (!__all_sync(0xffffffffu, mbar_try_wait(&empty[st], ph ^ 1))) {
           flush();
@@ -411,30 +473,21 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           if (!ok) break;
         }
         const uint32_t b = smem_u32(sB) + st * C::B_BYTES, sb = smem_u32(sSB) + st * C::SB_BYTES;
-        if (kRoute) {
-          const int c = lane & 7;  // 16-byte chunk of a 128-byte row
-          for (int r0 = 0; r0 < 2 * w.n; r0 += 4) {
-            const int r = r0 + (lane >> 3), i = r < w.n ? r : r - w.n;
-            const size_t row = __shfl_sync(0xffffffffu, my_row, i & 31);
-            const int to = r < w.n ? r : BN + i;  // row of the tile
-            if (r < 2 * w.n)
-              cp_async16(b + to * 128 + ((c ^ (to & 7)) << 4),
-                         (r < w.n ? src.hi : src.lo) + row * K + kc * 128 + c * 16);
-          }
-        } else if (lane == 0) {
-          mbar_arrive_expect_tx(&full[st], C::B_BYTES);
-          tma_load_2d(sB + st * C::B_BYTES, up ? &p.tm_xhi : &p.tm_hhi, &full[st], kc * 128,
-                      w.row0);
-          tma_load_2d(sB + st * C::B_BYTES + C::B_BYTES / 2, up ? &p.tm_xlo : &p.tm_hlo,
-                      &full[st], kc * 128, w.row0);
+        const int c = lane & 7;  // 16-byte chunk of a 128-byte row
+        for (int r0 = 0; r0 < 2 * w.n; r0 += 4) {
+          const int r = r0 + (lane >> 3), i = r < w.n ? r : r - w.n;
+          const size_t row = __shfl_sync(0xffffffffu, my_row, i & 31);
+          const int to = r < w.n ? r : BN + i;  // row of the tile
+          if (r < 2 * w.n)
+            cp_async16(b + to * 128 + ((c ^ (to & 7)) << 4),
+                       (r < w.n ? p.x.hi : p.x.lo) + row * K + kc * 128 + c * 16);
         }
         for (int r0 = 0; r0 < 2 * w.n; r0 += 32) {
           const int r = r0 + lane, i = r < w.n ? r : r - w.n;
-          const size_t row = kRoute ? __shfl_sync(0xffffffffu, my_row, i & 31) : w.row0 + i;
-          const int to = r < w.n ? r : BN + i;
+          const size_t row = __shfl_sync(0xffffffffu, my_row, i & 31);
           if (r < 2 * w.n)
-            cp_async4(sb + (to & 31) * 16 + (to >> 5) * 4,
-                      (r < w.n ? src.s_hi : src.s_lo) + row * ld + kc * 4);
+            cp_async4(sb + scale_row_at(r < w.n ? r : BN + i),
+                      p.xs + (row * nk + kc) * 8 + (r < w.n ? 0 : 4));
         }
         cp_async_commit();
         ++pending;
@@ -451,51 +504,57 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       if (!ok) break;
     }
     flush();
-    if (!ok && !kRoute && lane == 0) drain_stages(full, filled, S);
+    if (!ok && lane == 0) drain_stages(full, filled, S);
     __syncwarp();
   } else if (warp == 4) {
     // ---------------------------------------------------------------- MMA
+    // The warp stays together and one elected lane issues: with the operands of the instructions in
+    // uniform registers an issue takes a few clocks.  (Under `if (lane == 0)` each of a stage's 11
+    // tcgen05 operations took 70, twice the time of the products at 16 tokens.)
     int st = 0, it = 0;
     uint32_t ph = 0;
     Unit w;
-    bool ok = true;
-    while ((ok = next_unit(w, 36)) && w.kind >= 0) {
-      const int acc = it & 1, nk = (w.kind == 0 ? d : f) / 128;
-      const bool two = w.kind == 0 || (2 * w.mt + 1) * kMxTile < d;
-      if (lane == 0) {
-        ok = mbar_wait_suspend(&tempty[acc], ((it >> 1) & 1) ^ 1, abort_flag, p.b.status, 46);
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem_base);
+    const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB), sa_base = smem_u32(sSA),
+                   sb_base = smem_u32(sSB);
+    while (next_unit(w, 36)) {
+      const int kind = __reduce_max_sync(0xffffffffu, w.kind);
+      if (kind < 0) break;
+      const int acc = it & 1, nk = (kind == 0 ? d : f) / 128;
+      const bool two = kind == 0 || (2 * __reduce_max_sync(0xffffffffu, w.mt) + 1) * kMxTile < d;
+      bool ok = warp_wait(&tempty[acc], ((it >> 1) & 1) ^ 1, 46);
+      tc_fence_after();
+      const uint32_t d0 = tm + acc * C::ACC_COLS;
+      for (int kc = 0; ok && kc < nk; ++kc) {
+        ok = warp_wait(&full[st], ph, 37);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d0 = tmem_base + acc * C::ACC_COLS;
-        for (int kc = 0; ok && kc < nk; ++kc) {
-          ok = mbar_wait_suspend(&full[st], ph, abort_flag, p.b.status, 37);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sf = tmem_base + 2 * C::ACC_COLS + (kc & 1) * C::SF_COLS;
-          const uint32_t sa = smem_u32(sSA) + st * C::SA_BYTES;
+        const uint32_t sf = tm + 2 * C::ACC_COLS + (kc & 1) * C::SF_COLS;
+        const uint32_t sa = sa_base + st * C::SA_BYTES;
+        if (elect_one()) {
           tc_cp_scales(sf, sa);
           if (two) tc_cp_scales(sf + 4, sa + kMxScaleBlock);
-          tc_cp_scales(sf + 8, smem_u32(sSB) + st * C::SB_BYTES);
-          const uint32_t a = smem_u32(sA) + st * C::A_BYTES, b = smem_u32(sB) + st * C::B_BYTES;
+          tc_cp_scales(sf + 8, sb_base + st * C::SB_BYTES);
+          const uint64_t a = sdesc_k_sw128(a_base + st * C::A_BYTES),
+                         a2 = sdesc_k_sw128(a_base + st * C::A_BYTES + C::A_BYTES / 2),
+                         b = sdesc_k_sw128(b_base + st * C::B_BYTES);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
+          for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of a row: 2 units of the descriptors
             const uint32_t id = idesc_mx(kMxTile, N) | ((uint32_t)kk << 4) | ((uint32_t)kk << 29);
-            const uint64_t bd = sdesc_k_sw128(b + kk * 32);
             const uint32_t add = (kc | kk) ? 1u : 0u;
-            tc_mma_mx(d0, sdesc_k_sw128(a + kk * 32), bd, id, sf, sf + 8, add);
-            if (two)
-              tc_mma_mx(d0 + N, sdesc_k_sw128(a + C::A_BYTES / 2 + kk * 32), bd, id, sf + 4,
-                        sf + 8, add);
+            tc_mma_mx(d0, a + 2 * kk, b + 2 * kk, id, sf, sf + 8, add);
+            if (two) tc_mma_mx(d0 + N, a2 + 2 * kk, b + 2 * kk, id, sf + 4, sf + 8, add);
           }
           tc_commit(&empty[st]);
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
-          }
+          if (kc == nk - 1) tc_commit(&tfull[acc]);
         }
-        if (ok) tc_commit(&tfull[acc]);
+        __syncwarp();
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
+        }
       }
       ++it;
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
     }
     if (lane == 0) {
@@ -560,7 +619,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             }
             if (lane < 4 && (both || lane < 2)) {  // lanes 0, 1: first token; 2, 3: second
               const uint32_t s = lane < 2 ? sa : sb;
-              (lane & 1 ? p.h.s_lo : p.h.s_hi)[(row + (lane >> 1)) * act_scale_ld(f) + (col >> 5)] =
+              const int r = c + j + (lane >> 1);  // its row of the scale block, this warp's byte
+              p.hs[((size_t)w.tile * (f / 128) + w.mt) * kMxScaleBlock +
+                   scale_row_at(lane & 1 ? BN + r : r) + warp] =
                   (uint8_t)(lane & 1 ? lo_scale_byte(s) : s);
             }
           }

@@ -62,7 +62,15 @@ struct Unit {
   int g, mt, tok0, n, row0;
   int uses;  // token tiles of the group: how often its weights are read
   int rows;  // rows of the group
+  int tile;  // number of the token tile (token_tile_number)
 };
+
+// Token tile i (of bt rows) of group g, whose first sorted row is off, has number off / bt + g + i:
+// distinct for all tiles (a group of n rows moves the quotient by n / bt at least, rounded down,
+// and g by one), below rows / bt + groups.
+__host__ __device__ __forceinline__ int token_tile_number(int off, int g, int i, int bt) {
+  return off / bt + g + i;
+}
 
 // mbar_wait_bounded with long suspended tries: a dozen warps that poll would take the issue
 // slots of those that work.
@@ -275,7 +283,9 @@ __device__ __forceinline__ void schedule_units(const StreamBase &p, const Stream
       r.tok0 = (loc - r.mt * r.uses) * bt;
       r.rows = group_rows(p, tb, r.g);
       r.n = min(bt, r.rows - r.tok0);
-      r.row0 = (r.g < p.E ? tb.offsets[r.g] : p.T * p.k) + r.tok0;
+      const int off = r.g < p.E ? tb.offsets[r.g] : p.T * p.k;
+      r.row0 = off + r.tok0;
+      r.tile = token_tile_number(off, r.g, r.tok0 / bt, bt);
     }
     if (!mbar_wait_suspend(&uq_empty[qi], qph ^ 1, abort_flag, p.status, 31)) break;
     uq[qi] = r;

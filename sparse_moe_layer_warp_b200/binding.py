@@ -6,6 +6,7 @@ the shared library is missing or fails to load, importing the functions raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -169,6 +170,15 @@ def _p(t):
 def _stream(stream):
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _on_device_of(t):
+    """Context in which t's device is current (entering one costs more than a small launch)."""
+    dev = t.get_device()
+    return _SAME_DEVICE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 # ------------------------------------------------------------------ C-ABI mirrors
@@ -439,10 +449,10 @@ def mxfp4_quantize(w, stream=None):
                          f"{tuple(w.shape)}")
     _addr(w)
     lead, cols = tuple(w.shape[:-1]), int(w.shape[-1])
-    codes = torch.empty(lead + (cols // 2,), dtype=torch.uint8, device=w.device)
-    scales = torch.empty(lead + (cols // MXFP4_BLOCK,), dtype=torch.uint8, device=w.device)
+    codes = w.new_empty(lead + (cols // 2,), dtype=torch.uint8)
+    scales = w.new_empty(lead + (cols // MXFP4_BLOCK,), dtype=torch.uint8)
     if w.numel():
-        with torch.cuda.device(w.device):
+        with _on_device_of(w):
             moe_mxfp4_quantize(w, codes, scales, stream)
     return codes, scales
 
@@ -460,9 +470,9 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
     _addr(codes)
     if scales.device != codes.device:
         raise ValueError(f"scales: on {scales.device}, codes on {codes.device}")
-    out = torch.empty(lead + (cols,), dtype=dtype, device=codes.device)
+    out = codes.new_empty(lead + (cols,), dtype=dtype)
     if out.numel():
-        with torch.cuda.device(codes.device):
+        with _on_device_of(codes):
             moe_mxfp4_dequantize(codes, scales, out, stream)
     return out
 

@@ -34,6 +34,7 @@
 #include "grouped_gemm_pair.cuh"
 #include "mxfp4.cuh"
 #include "mxfp4_layer.cuh"
+#include "mxfp4_pair.cuh"
 #include "ptx_sm100.cuh"
 #include "router_stats.cuh"
 #include "routing.cuh"
@@ -74,7 +75,7 @@ struct moe_layer {
   cudaStream_t side;
   cudaEvent_t ev_fork, ev_join;
   // MXFP4 expert weights (moe_layer_init_mxfp4): w holds the codes, these the scales
-  int mx;
+  int mx, mx_pair_grid;
   const uint8_t *sc_gate, *sc_up, *sc_down;
   // the expert weights as the weight-streaming kernel loads them (bf16 or code bytes)
   CUtensorMap tm_st_g, tm_st_u, tm_st_d;
@@ -143,6 +144,21 @@ bool encode_codes(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows
   cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void *>(base), dims, strides,
             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// Row-major bytes [rows, cols] -> map with box {128 bytes, box_rows rows} and 128-byte swizzle.
+bool encode_u8_2d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows,
+                  uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
@@ -253,7 +269,7 @@ bool few_shape(const moe_config &c, int T) {
 // Token rows of a tile of the MXFP4 layer.
 int mx_token_tile(const moe_config &c, int T) {
   if (few_shape(c, T)) return T <= 8 ? 8 : (T <= 16 ? 16 : 32);
-  return (long long)T * c.top_k <= 16ll * c.n_experts ? 32 : 56;
+  return (long long)T * c.top_k <= 16ll * c.n_experts ? 32 : kMxPairBN;
 }
 
 // mx: an MXFP4 handle's layout (x and h as pairs of e4m3 values with their scales; x by token for
@@ -292,9 +308,10 @@ WsLayout ws_layout(const moe_config &c, int T, bool mx = false) {
   const size_t x_rows = !mx ? 0 : few_shape(c, T) ? (size_t)T : P;
   L.x_split = take(2 * x_rows * c.d_model);
   // scale blocks of every token tile (x of the one-launch layer: words by token)
+  const size_t block = scale_block_bytes(mx_token_tile(c, T));
   const size_t tiles = !mx ? 0 : P / mx_token_tile(c, T) + c.n_experts + c.n_shared;
-  L.x_scale = take((few_shape(c, T) ? x_rows * 8 : tiles * kMxScaleBlock) * (c.d_model / 128));
-  L.h_scale = take(tiles * kMxScaleBlock * (c.d_ff / 128));
+  L.x_scale = take((few_shape(c, T) ? x_rows * 8 : tiles * block) * (c.d_model / 128));
+  L.h_scale = take(tiles * block * (c.d_ff / 128));
   L.total = off;
   return L;
 }
@@ -823,6 +840,12 @@ static moe_status layer_init(const moe_config *cfg, const moe_weights *w, int e0
     const uint64_t G = (uint64_t)(e1 - e0) + c.n_shared;  // weight groups held
     if (mx) {
       L->mx = 1;
+      L->mx_pair_grid =
+          cluster_grid_size(mxfp4_pair_kernel, MxPairCfg::SMEM, kMxPairThreads, L);
+      if (L->mx_pair_grid < 2) {
+        free(L);
+        return MOE_ERR_CUDA;
+      }
       L->sc_gate = mx->scale_gate;
       L->sc_up = mx->scale_up;
       L->sc_down = mx->scale_down;
@@ -877,7 +900,7 @@ moe_status moe_layer_init_mxfp4(const moe_config *cfg, const moe_mxfp4_weights *
   if (cfg->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   // counts of finished pieces of h are 32-bit
   if (cfg->max_tokens > 0 && cfg->d_ff > 0 && cfg->top_k > 0 &&
-      (double)cfg->max_tokens * (cfg->top_k + 1) * (cfg->d_ff / 32) >= 2147483648.0)
+      (double)cfg->max_tokens * (cfg->top_k + 1) * (cfg->d_ff / 32 + 8) >= 2147483648.0)
     return MOE_ERR_UNSUPPORTED;
   if (!w->scale_gate || !w->scale_up || !w->scale_down) return MOE_ERR_INVALID_ARG;
   if (!aligned16(w->scale_gate) || !aligned16(w->scale_up) || !aligned16(w->scale_down) ||
@@ -1532,6 +1555,49 @@ moe_status launch_mx(const moe_layer *L, const void *x, int T, void *out, void *
                        st);
 }
 
+// 512-byte scale blocks [n] as words -> map with box {a block's 128 words, box_blocks}.
+bool encode_scale_blocks(CUtensorMap *m, const void *base, uint64_t n, uint32_t box_blocks) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {kMxScaleBlock / 4, n};
+  cuuint64_t strides[1] = {kMxScaleBlock};
+  cuuint32_t box[2] = {kMxScaleBlock / 4, box_blocks};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// MXFP4 layer on CTA pairs.
+moe_status launch_mx_pair(const moe_layer *L, const void *x, int T, void *out, void *ws,
+                          const WsLayout &W, cudaStream_t st) {
+  const moe_config &c = L->cfg;
+  const size_t P = (size_t)T * (c.top_k + c.n_shared), G = (size_t)c.n_experts + c.n_shared;
+  const size_t tiles = P / kMxPairBN + G, wblocks = G * (c.d_ff / 128) * (c.d_model / 128);
+  MxPairParams p;
+  memset(&p, 0, sizeof p);
+  p.b = stream_base(L, x, T, out, ws, W);
+  p.tm_g = L->tm_st_g;
+  p.tm_u = L->tm_st_u;
+  p.tm_d = L->tm_st_d;
+  const uint8_t *xs = at<uint8_t>(ws, W.x_split);
+  p.h = split_rows(at<uint8_t>(ws, W.h), P, c.d_ff);
+  p.hs = at<uint8_t>(ws, W.h_scale);
+  bool ok = encode_scale_blocks(&p.tm_sg, L->sc_gate, wblocks, 1) &&
+            encode_scale_blocks(&p.tm_su, L->sc_up, wblocks, 1) &&
+            encode_scale_blocks(&p.tm_sd, L->sc_down, wblocks, 1) &&
+            encode_scale_blocks(&p.tm_xs, at<uint8_t>(ws, W.x_scale),
+                                tiles * 2 * (c.d_model / 128), 2) &&
+            encode_scale_blocks(&p.tm_hs, p.hs, tiles * 2 * (c.d_ff / 128), 2);
+  for (int i = 0; i < 2; ++i)
+    ok = ok && encode_u8_2d(&p.tm_x[i], xs, c.d_model, 2 * P, 56u << i) &&
+         encode_u8_2d(&p.tm_h[i], p.h.hi, c.d_ff, 2 * P, 56u << i);
+  if (!ok) return MOE_ERR_CUDA;
+  return launch_cl(mxfp4_pair_kernel, dim3(L->mx_pair_grid), dim3(kMxPairThreads), MxPairCfg::SMEM,
+                   st, 2, p);
+}
+
 template <int NT>
 moe_status launch_bf16_few(const moe_layer *L, const void *x, int T, void *out, void *ws,
                            const WsLayout &W, cudaStream_t st) {
@@ -1587,7 +1653,7 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
                   at<uint8_t>(ws, W.x_scale))) != MOE_OK)
     return s;
   return mx_token_tile(c, T) == 32 ? launch_mx<32, false>(L, x, T, out, ws, W, st)
-                                   : launch_mx<56, false>(L, x, T, out, ws, W, st);
+                                   : launch_mx_pair(L, x, T, out, ws, W, st);
 }
 
 int mxfp4_launches(const moe_layer *L, int T) {

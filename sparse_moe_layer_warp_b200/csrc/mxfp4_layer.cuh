@@ -45,9 +45,19 @@ __host__ __forceinline__ SplitRows split_rows(uint8_t *values, size_t rows, int 
   return {values, values + rows * cols};
 }
 
-// Their scales come in blocks as the weights' do, one for each token tile of BN rows and 128
-// columns (token_tile_number): rows 0 .. BN - 1 of a block are hi's, BN .. 2 BN - 1 lo's.
-__device__ __forceinline__ int scale_row_at(int r) { return (r & 31) * 16 + (r >> 5) * 4; }
+// Their scales come in blocks as the weights' do, one (or two, one behind the other, past 128 rows)
+// for each token tile and 128 columns (token_tile_number): of a tile with n tokens, rows 0 .. n - 1
+// are hi's; lo's begin at row BN, or on CTA pairs, whose N follows n, at the next multiple of 8.
+constexpr int kMxPairBN = 112;  // token rows of a CTA pair's tile (mxfp4_pair.cuh)
+__host__ __device__ constexpr int scale_block_bytes(int BN) {
+  return (2 * BN + 127) / 128 * kMxScaleBlock;
+}
+__device__ __forceinline__ int scale_lo_row(int n, int BN) {
+  return BN == kMxPairBN ? (n + 7) & ~7 : BN;
+}
+__device__ __forceinline__ int scale_row_at(int r) {
+  return (r >> 7) * kMxScaleBlock + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+}
 
 struct MxParams {
   StreamBase b;
@@ -64,7 +74,7 @@ struct MxCfg {
   static constexpr int N = 2 * BN;                 // MMA N: hi rows, lo rows
   static constexpr int A_BYTES = 2 * kMxTile * 128;
   static constexpr int B_BYTES = N * 128;
-  static constexpr int SA_BYTES = 2 * kMxScaleBlock, SB_BYTES = kMxScaleBlock;
+  static constexpr int SA_BYTES = 2 * kMxScaleBlock, SB_BYTES = scale_block_bytes(BN);
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
   static constexpr int ACC_COLS = 2 * N;           // both weight tiles
   static constexpr int SF_COLS = 16;               // scale columns of a stage; two sets in turn
@@ -107,12 +117,13 @@ __device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t a, uint64_t b, ui
 }
 // One 512-byte scale block -> 4 TMEM columns of all four lane quadrants (rows of 16 bytes, groups
 // of 8 rows 128 bytes apart, no swizzle).  Runs in order with the thread's MMAs.
+__device__ __forceinline__ uint64_t scale_block_desc(uint32_t smem_addr) {
+  return (uint64_t)((smem_addr >> 4) & 0x3FFFu) | (uint64_t)(128u >> 4) << 32 | (uint64_t)1u << 46;
+}
 __device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)(128u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+               "l"(scale_block_desc(smem_addr))
+               : "memory");
 }
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -183,6 +194,38 @@ __device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[16]) {
   }
 }
 
+// Eight tokens (c .. c + 7 of a tile of n) x a warp's 32 columns of h, from the sums of gate and up,
+// as split values with the scale byte k of their rows: col the first column, hs the tile's scale
+// block of these 128 columns, lo0 the block's first lo row.
+__device__ __forceinline__ void store_h_chunk(const SplitRows &h, uint8_t *hs, int f, int row0,
+                                              int col, int c, int n, int lo0, int k, int lane,
+                                              const float (&gate)[8], const float (&up)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    if (c + j >= n) break;
+    const float ha = swiglu(gate[j], up[j]), hb = swiglu(gate[j + 1], up[j + 1]);
+    const uint32_t sa =
+        act_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(ha) & 0x7fffffffu));
+    const uint32_t sb =
+        act_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(hb) & 0x7fffffffu));
+    uint32_t hi, lo;
+    split_pair(ha, hb, sa, sb, hi, lo);
+    const size_t at = (size_t)(row0 + c + j) * f + col + lane;
+    h.hi[at] = (uint8_t)hi;
+    h.lo[at] = (uint8_t)lo;
+    const bool both = c + j + 1 < n;
+    if (both) {
+      h.hi[at + f] = (uint8_t)(hi >> 8);
+      h.lo[at + f] = (uint8_t)(lo >> 8);
+    }
+    if (lane < 4 && (both || lane < 2)) {  // lanes 0, 1: first token; 2, 3: second
+      const uint32_t s = lane < 2 ? sa : sb;
+      const int r = c + j + (lane >> 1);
+      hs[scale_row_at(lane & 1 ? lo0 + r : r) + k] = (uint8_t)(lane & 1 ? lo_scale_byte(s) : s);
+    }
+  }
+}
+
 // x [T, d] -> the split rows of the sorted space with their scale blocks: token t to its k routed
 // rows and its shared row.  One warp a token: converts 512 columns at a time and stores them
 // k + n_shared times; bound by HBM (2 d bytes read, 2 d (k + n_shared) written a token).
@@ -194,14 +237,15 @@ __global__ void __launch_bounds__(256)
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, nk = d / 128, n_warps = gridDim.x * 8;
   for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += n_warps) {
-    // lane j: row of slot j (the shared row last), its tile's scale blocks, its place in a block
-    int row = 0, tile = 0, r = 0;
+    // lane j: row of slot j (the shared row last), its tile's number, its hi and lo rows in a block
+    int row = 0, tile = 0, r = 0, r_lo = 0;
     if (lane < k + n_shared) {
       const int g = lane < k ? idx[(size_t)t * k + lane] : E;
-      const int off = lane < k ? offsets[g] : T * k;
+      const int off = lane < k ? offsets[g] : T * k, rows = lane < k ? offsets[g + 1] - off : T;
       row = lane < k ? slot_row[(size_t)t * k + lane] : T * k + t;
       tile = token_tile_number(off, g, (row - off) / BN, BN);
       r = (row - off) % BN;
+      r_lo = scale_lo_row(min(BN, rows - (row - off - r)), BN) + r;
     }
     for (int c0 = 0; c0 < d; c0 += 512) {
       const int c = c0 + lane * 16;
@@ -215,13 +259,13 @@ __global__ void __launch_bounds__(256)
       for (int j = 0; j < k + n_shared; ++j) {
         const size_t rw = __shfl_sync(0xffffffffu, row, j);
         const size_t tl = __shfl_sync(0xffffffffu, tile, j);
-        const int rj = __shfl_sync(0xffffffffu, r, j);
+        const int rj = __shfl_sync(0xffffffffu, r, j), lj = __shfl_sync(0xffffffffu, r_lo, j);
         if (c >= d) continue;
         *reinterpret_cast<uint4 *>(out.hi + rw * d + c) = hi;
         *reinterpret_cast<uint4 *>(out.lo + rw * d + c) = lo;
         if ((lane & 7) < 2)
-          *reinterpret_cast<uint32_t *>(xs + (tl * nk + (c >> 7)) * kMxScaleBlock +
-                                        scale_row_at((lane & 1) ? BN + rj : rj)) =
+          *reinterpret_cast<uint32_t *>(xs + (tl * nk + (c >> 7)) * scale_block_bytes(BN) +
+                                        scale_row_at((lane & 1) ? lj : rj)) =
               (lane & 1) ? s_lo : s_hi;
       }
     }
@@ -340,7 +384,18 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     // the grid barrier gave up: no unit is claimed
   } else if (warp == 8) {
     if (lane == 0)
-      schedule_units(p.b, tb, BN, up_tiles, down_tiles, uq, uq_full, uq_empty, abort_flag);
+      schedule_units(p.b, tb, BN, up_tiles, down_tiles, blockIdx.x, gridDim.x,
+                     [&](const Unit &r) {
+                       if (!mbar_wait_suspend(&uq_empty[qi], qph ^ 1, abort_flag, p.b.status, 31))
+                         return false;
+                       uq[qi] = r;
+                       mbar_arrive(&uq_full[qi]);
+                       if (++qi == kUnitQ) {
+                         qi = 0;
+                         qph ^= 1;
+                       }
+                       return true;
+                     });
     __syncwarp();
   } else if (warp == 5 || warp == 6) {
     // ---------------------------------------------------------------- weights
@@ -442,13 +497,13 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         flush();
         if (lane == 0) {
           const CUtensorMap *m = up ? &p.tm_x : &p.tm_h;
-          const uint8_t *sc = (up ? p.xs : p.hs) + (size_t)w.tile * nk * kMxScaleBlock;
+          const uint8_t *sc = (up ? p.xs : p.hs) + (size_t)w.tile * nk * C::SB_BYTES;
           for (int kc = 0; kc < nk; ++kc) {
             ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 35);
             if (!ok) break;
-            mbar_arrive_expect_tx(&full[st], C::B_BYTES + kMxScaleBlock);
+            mbar_arrive_expect_tx(&full[st], C::B_BYTES + C::SB_BYTES);
             tma_load_3d(sB + st * C::B_BYTES, m, &full[st], kc * 128, w.row0, 0);
-            bulk_load(sSB + st * C::SB_BYTES, sc + kc * kMxScaleBlock, kMxScaleBlock, &full[st]);
+            bulk_load(sSB + st * C::SB_BYTES, sc + kc * C::SB_BYTES, C::SB_BYTES, &full[st]);
             ++filled;
             if (++st == S) {
               st = 0;
@@ -598,33 +653,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           v1[j] = two ? __uint_as_float(r2[j]) + __uint_as_float(r3[j]) : 0.f;
         }
         if (up) {
-          const int col = w.mt * kMxTile + warp * 32;  // a block of 32 columns of h
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            if (c + j >= w.n) break;
-            const float ha = swiglu(v0[j], v1[j]), hb = swiglu(v0[j + 1], v1[j + 1]);
-            const uint32_t sa = act_scale_byte(
-                __reduce_max_sync(0xffffffffu, __float_as_uint(ha) & 0x7fffffffu));
-            const uint32_t sb = act_scale_byte(
-                __reduce_max_sync(0xffffffffu, __float_as_uint(hb) & 0x7fffffffu));
-            uint32_t hi, lo;
-            split_pair(ha, hb, sa, sb, hi, lo);
-            const size_t row = w.row0 + c + j, at = row * f + col + lane;
-            p.h.hi[at] = (uint8_t)hi;
-            p.h.lo[at] = (uint8_t)lo;
-            const bool both = c + j + 1 < w.n;
-            if (both) {
-              p.h.hi[at + f] = (uint8_t)(hi >> 8);
-              p.h.lo[at + f] = (uint8_t)(lo >> 8);
-            }
-            if (lane < 4 && (both || lane < 2)) {  // lanes 0, 1: first token; 2, 3: second
-              const uint32_t s = lane < 2 ? sa : sb;
-              const int r = c + j + (lane >> 1);  // its row of the scale block, this warp's byte
-              p.hs[((size_t)w.tile * (f / 128) + w.mt) * kMxScaleBlock +
-                   scale_row_at(lane & 1 ? BN + r : r) + warp] =
-                  (uint8_t)(lane & 1 ? lo_scale_byte(s) : s);
-            }
-          }
+          store_h_chunk(p.h, p.hs + ((size_t)w.tile * (f / 128) + w.mt) * C::SB_BYTES, f, w.row0,
+                        w.mt * kMxTile + warp * 32, c, w.n, BN, warp, lane, v0, v1);
         } else {
           float *y = p.b.y + (size_t)(w.row0 + c) * d + w.mt * kMxDown + warp * 32 + lane;
 #pragma unroll

@@ -1,0 +1,400 @@
+// mxfp4_pair.cuh -- the experts over MXFP4 weights on CTA pairs (tcgen05 cta_group::2), for groups of
+// many tokens.  Arithmetic, units and waits are mxfp4_layer.cuh's.
+//
+// What bounds mxfp4_layer_kernel there is shared memory: a stage of two 128-row weight tiles and
+// 56 tokens takes 448 clocks of tensor time, but its operands cross the 128 bytes a clock of shared
+// memory for 830 (codes are one byte there; they are written by the copy, and read once for every
+// 112 columns of N).  A pair runs M = 256, N = 224: a CTA's codes are read once for 112 tokens, and
+// each CTA holds and reads only half of the token rows -- the hi rows in the leader, the lo rows in
+// its peer.  A stage of 896 clocks then moves 106 KB: the tensor cores bind again.
+//
+// CTA r of a pair holds weight rows [128 r, 128 r + 128) of each 256-row tile; a unit has two tiles
+// (gate and up; two neighbours of W_d).  N follows the unit's tokens (2 x the next multiple of 8).
+// TMEM: 2 x 224 accumulator columns, so one unit at a time; two sets of scales.  The scales of all N
+// columns are needed by both CTAs, those of the weight rows by the CTA that holds them.
+#pragma once
+#include "mxfp4_layer.cuh"
+
+namespace moe {
+
+constexpr int kMxPairEpiWarps = 8;  // warps 0-7: two for each TMEM lane quadrant
+constexpr int kMxPairThreads = 32 * 16;  // 8 MMA, 9-10 weights, 11 token rows, 12 scheduler
+
+struct MxPairParams {
+  StreamBase b;
+  CUtensorMap tm_g, tm_u, tm_d;      // codes, box {128, 128}, padded 4-bit
+  CUtensorMap tm_sg, tm_su, tm_sd;   // their scale blocks as words, box {128, 1}
+  CUtensorMap tm_x[2], tm_h[2];      // token rows, hi then lo [2 P, cols]: box 56 or 112 rows
+  CUtensorMap tm_xs, tm_hs;          // scale blocks as words, box {128, 2}
+  SplitRows h;
+  uint8_t *hs;
+};
+
+struct MxPairCfg {
+  static constexpr int BN = kMxPairBN;
+  static constexpr int A_BYTES = 2 * kMxTile * 128;
+  static constexpr int B_BYTES = BN * 128;  // hi rows (leader) or lo rows (peer)
+  static constexpr int SA_BYTES = 2 * kMxScaleBlock, SB_BYTES = scale_block_bytes(BN);
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
+  static constexpr int TILE_COLS = 2 * BN, ACC_COLS = 2 * TILE_COLS;
+  static constexpr int SF_COLS = 16;  // weights 2 x 4, tokens 8
+  static constexpr int TMEM_COLS = 512;
+  static_assert(ACC_COLS + 2 * SF_COLS <= TMEM_COLS && SB_BYTES == 1024, "TMEM");
+  static constexpr int FIXED = StreamTables::BYTES + 1024 /*barriers*/ + 1024 /*alignment*/;
+  static constexpr int STAGES = (226 * 1024 - FIXED) / STAGE_BYTES;
+  static_assert(STAGES >= 4 && B_BYTES % 1024 == 0, "pipeline");
+  static constexpr size_t SMEM = FIXED + (size_t)STAGES * STAGE_BYTES;
+};
+
+__device__ __forceinline__ void tc_mma_mx_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t sf_a, uint32_t sf_b, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+          d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sf_a), "r"(sf_b)
+      : "memory");
+}
+// one scale block in each CTA of the pair, to the same TMEM columns of each
+__device__ __forceinline__ void tc_cp_scales_pair(uint32_t taddr, uint32_t smem_addr) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr),
+               "l"(scale_block_desc(smem_addr))
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kMxPairThreads, 1)
+    mxfp4_pair_kernel(const __grid_constant__ MxPairParams p) {
+  using C = MxPairCfg;
+  constexpr int S = C::STAGES, BN = C::BN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t *sA = smem;                       // [S][2 tiles][128 rows][128 B]
+  uint8_t *sB = sA + S * C::A_BYTES;        // [S][BN rows][128 B]
+  uint8_t *sSA = sB + S * C::B_BYTES;       // [S][2][512]
+  uint8_t *sSB = sSA + S * C::SA_BYTES;     // [S][1024]
+  uint64_t *full = reinterpret_cast<uint64_t *>(sSB + S * C::SB_BYTES);  // the leader's: both CTAs'
+  uint64_t *empty = full + S;
+  uint64_t *tfull = empty + S;
+  uint64_t *tempty = tfull + 1;             // the leader's: both CTAs' epilogue warps
+  uint64_t *uq_full = tempty + 1;
+  uint64_t *uq_empty = uq_full + kUnitQ;    // the leader's: both CTAs' readers
+  uint64_t *mma_end = uq_empty + kUnitQ;
+  Unit *uq = reinterpret_cast<Unit *>(mma_end + 1);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(uq + kUnitQ);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  const StreamTables tb(reinterpret_cast<uint8_t *>(full) + 1024, p.b.E, p.b.n_shared);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int Tk = p.b.T * p.b.k, d = p.b.d, f = p.b.f;
+  const int up_tiles = (f + 255) / 256, down_tiles = (d + 511) / 512;
+  const int n_rows = Tk + p.b.n_shared * p.b.T;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 3);  // the leader's three producer warps
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 2 * kMxPairEpiWarps);
+    for (int q = 0; q < kUnitQ; ++q) {
+      mbar_init(&uq_full[q], 1);
+      mbar_init(&uq_empty[q], 2 * (kMxPairEpiWarps + 3) + 1);
+    }
+    mbar_init(mma_end, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_g);
+    tma_prefetch_desc(&p.tm_u);
+    tma_prefetch_desc(&p.tm_d);
+  }
+  if (warp == 8) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int e = threadIdx.x; e <= p.b.E; e += blockDim.x) tb.offsets[e] = p.b.offsets[e];
+  __syncthreads();
+  if (warp == 0) build_tile_prefix(p.b, tb, BN);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised, their TMEM allocated
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  auto warp_wait = [&](uint64_t *bar, uint32_t parity, int where) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait_suspend(bar, parity, abort_flag, p.b.status, where));
+  };
+  int qi = 0;
+  uint32_t qph = 0;
+  const uint32_t uq_empty_leader = mapa_shared(smem_u32(uq_empty), 0);
+  auto next_unit = [&](Unit &w, int where) -> bool {
+    if (!__all_sync(0xffffffffu, mbar_wait_suspend<true>(&uq_full[qi], qph, abort_flag,
+                                                         p.b.status, where)))
+      return false;
+    w = uq[qi];
+    __syncwarp();
+    if (lane == 0) mbar_arrive_remote(uq_empty_leader + qi * 8);
+    if (++qi == kUnitQ) {
+      qi = 0;
+      qph ^= 1;
+    }
+    return true;
+  };
+  // first row (of the group's weights) of tile j of a unit in CTA r
+  auto tile_row = [&](const Unit &w, int j, int r) {
+    return w.kind == 0 ? w.mt * 256 + r * kMxTile : w.mt * 512 + j * 256 + r * kMxTile;
+  };
+  bool alive = true;
+
+  if (warp == 12) {
+    if (lane == 0 && leader)
+      schedule_units(p.b, tb, BN, up_tiles, down_tiles, blockIdx.x >> 1, gridDim.x >> 1,
+                     [&](const Unit &r) {
+                       if (!mbar_wait_suspend<true>(&uq_empty[qi], qph ^ 1, abort_flag, p.b.status,
+                                                    31))
+                         return false;
+                       uq[qi] = r;
+                       const uint32_t to = mapa_shared(smem_u32(&uq[qi]), 1);
+                       const int *v = reinterpret_cast<const int *>(&r);
+#pragma unroll
+                       for (int i = 0; i < (int)(sizeof(Unit) / 4); ++i)
+                         st_shared_remote(to + 4 * i, v[i]);
+                       mbar_arrive(&uq_full[qi]);
+                       mbar_arrive_remote(mapa_shared(smem_u32(&uq_full[qi]), 1));
+                       if (++qi == kUnitQ) {
+                         qi = 0;
+                         qph ^= 1;
+                       }
+                       return true;
+                     });
+    __syncwarp();
+  } else if (warp == 9 || warp == 10) {
+    // ---------------------------------------------------------------- weights (tile j)
+    const int j = warp - 9;
+    const uint64_t pol_once = policy_evict_first(), pol_reuse = policy_evict_last();
+    int st = 0, filled = 0;
+    uint32_t ph = 0;
+    Unit w;
+    bool ok = true;
+    while ((ok = next_unit(w, 45)) && w.kind >= 0) {
+      if (lane == 0) {
+        const bool up = w.kind == 0;
+        const int nk = (up ? d : f) / 128, m_rows = up ? f : d;
+        const bool there = tile_row(w, j, rank) < m_rows;
+        const int row = w.g * m_rows + tile_row(w, j, rank);
+        const uint32_t bytes = ((tile_row(w, j, 0) < m_rows) + (tile_row(w, j, 1) < m_rows)) *
+                               (kMxTile * 64 + kMxScaleBlock);  // of both CTAs
+        const CUtensorMap *m = up ? (j ? &p.tm_u : &p.tm_g) : &p.tm_d;
+        const CUtensorMap *sc = up ? (j ? &p.tm_su : &p.tm_sg) : &p.tm_sd;
+        const uint64_t pol = w.uses == 1 ? pol_once : pol_reuse;
+        for (int kc = 0; kc < nk; ++kc) {
+          ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 32);
+          if (!ok) break;
+          if (leader) {
+            if (bytes) mbar_arrive_expect_tx(&full[st], bytes);
+            else mbar_arrive(&full[st]);
+          }
+          if (there) {
+            const uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
+            tma_load_2d_pair(sA + st * C::A_BYTES + j * (C::A_BYTES / 2), m, bar, kc * 128, row,
+                             pol);
+            tma_load_2d_pair(sSA + st * C::SA_BYTES + j * kMxScaleBlock, sc, bar, 0,
+                             row / kMxTile * nk + kc, pol);
+          }
+          ++filled;
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+    }
+    if (!ok && lane == 0 && leader) drain_stages(full, filled, S);
+    __syncwarp();
+  } else if (warp == 11) {
+    // ---------------------------------------------------------------- token rows
+    const int h_target = n_rows * up_tiles * 8;
+    const uint64_t pol = policy_evict_last();
+    bool all_ready = false;
+    int st = 0, filled = 0;
+    uint32_t ph = 0;
+    Unit w;
+    bool ok = true;
+    while ((ok = next_unit(w, 33)) && w.kind >= 0) {
+      if (lane == 0) {
+        const bool up = w.kind == 0;
+        if (!up && !all_ready) {
+          ok = counter_wait_bounded(p.b.done + w.g, w.rows * up_tiles * 8, abort_flag, p.b.status,
+                                    34);
+          all_ready = counter_load(p.b.done_all) == h_target;
+          fence_proxy_async_global();  // other CTAs' stores, read by TMA
+        }
+        const int nk = (up ? d : f) / 128, box = w.n > 56 ? 1 : 0;
+        const CUtensorMap *m = up ? &p.tm_x[box] : &p.tm_h[box], *sc = up ? &p.tm_xs : &p.tm_hs;
+        for (int kc = 0; ok && kc < nk; ++kc) {
+          ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 35);
+          if (!ok) break;
+          const uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
+          if (leader)
+            mbar_arrive_expect_tx(&full[st], 2 * ((box ? 112 : 56) * 128 + C::SB_BYTES));
+          tma_load_2d_pair(sB + st * C::B_BYTES, m, bar, kc * 128, (int)rank * n_rows + w.row0,
+                           pol);
+          tma_load_2d_pair(sSB + st * C::SB_BYTES, sc, bar, 0, (w.tile * nk + kc) * 2, pol);
+          ++filled;
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) break;
+    }
+    if (!ok && lane == 0 && leader) drain_stages(full, filled, S);
+    __syncwarp();
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- MMA (leader)
+    if (leader) {
+      int st = 0, it = 0;
+      uint32_t ph = 0;
+      Unit w;
+      const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem_base);
+      const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB), sa_base = smem_u32(sSA),
+                     sb_base = smem_u32(sSB);
+      while (next_unit(w, 36)) {
+        const int kind = __reduce_max_sync(0xffffffffu, w.kind);
+        if (kind < 0) break;
+        const int nk = (kind == 0 ? d : f) / 128;
+        const int half = scale_lo_row(__reduce_max_sync(0xffffffffu, w.n), BN);
+        const bool two = kind == 0 || __reduce_max_sync(0xffffffffu, w.mt) * 512 + 256 < d;
+        bool ok = warp_wait(tempty, (it & 1) ^ 1, 46);
+        ++it;
+        tc_fence_after();
+        for (int kc = 0; ok && kc < nk; ++kc) {
+          ok = warp_wait(&full[st], ph, 37);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sf = tm + C::ACC_COLS + (kc & 1) * C::SF_COLS;
+          const uint32_t sa = sa_base + st * C::SA_BYTES, sb = sb_base + st * C::SB_BYTES;
+          if (elect_one()) {
+            tc_cp_scales_pair(sf, sa);
+            if (two) tc_cp_scales_pair(sf + 4, sa + kMxScaleBlock);
+            tc_cp_scales_pair(sf + 8, sb);
+            if (half > 64) tc_cp_scales_pair(sf + 12, sb + kMxScaleBlock);
+            const uint64_t a = sdesc_k_sw128(a_base + st * C::A_BYTES),
+                           a2 = sdesc_k_sw128(a_base + st * C::A_BYTES + C::A_BYTES / 2),
+                           b = sdesc_k_sw128(b_base + st * C::B_BYTES);
+            const uint32_t id0 = idesc_mx(256, 2 * half);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t id = id0 | ((uint32_t)kk << 4) | ((uint32_t)kk << 29);
+              const uint32_t add = (kc | kk) ? 1u : 0u;
+              tc_mma_mx_pair(tm, a + 2 * kk, b + 2 * kk, id, sf, sf + 8, add);
+              if (two) tc_mma_mx_pair(tm + C::TILE_COLS, a2 + 2 * kk, b + 2 * kk, id, sf + 4,
+                                      sf + 8, add);
+            }
+            tc_commit_pair_both(&empty[st]);
+            if (kc == nk - 1) tc_commit_pair_both(tfull);
+          }
+          __syncwarp();
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+      }
+      if (lane == 0) {
+        tc_commit_pair_local(mma_end);
+        volatile int no_abort = 0;
+        mbar_wait_bounded(mma_end, 0, &no_abort, nullptr, 0);
+      }
+    }
+    __syncwarp();
+  } else if (warp < kMxPairEpiWarps) {
+    // ---------------------------------------------------------------- epilogue
+    // Chunks of 8 tokens, alternating between the two warps of a quadrant.
+    const int q = warp & 3, eh = warp >> 2;
+    const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
+    int it = 0;
+    Unit w;
+    while ((alive = next_unit(w, 42)) && w.kind >= 0) {
+      const bool up = w.kind == 0;
+      const int m_rows = up ? f : d, half = scale_lo_row(w.n, BN);
+      const int row_a = tile_row(w, 0, rank), row_b = tile_row(w, 1, rank);
+      const bool one = row_a < m_rows, two = row_b < m_rows;
+      // down: routed_scale * gate of this warp's tokens (lane, lane + 32), asked for before the wait
+      float sc0 = 1.f, sc1 = 1.f;
+      if (!up && w.g < p.b.E) {
+        const int i0 = (lane >> 3) * 16 + eh * 8 + (lane & 7), i1 = i0 + 64;
+        if (i0 < w.n) sc0 = p.b.routed_scale * p.b.gate[p.b.perm[w.row0 + i0]];
+        if (i1 < w.n) sc1 = p.b.routed_scale * p.b.gate[p.b.perm[w.row0 + i1]];
+      }
+      alive = warp_wait(tfull, it & 1, 39);
+      if (!alive) break;
+      ++it;
+      tc_fence_after();
+      const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16);
+      int count = 0;
+      for (int c = 8 * eh; c < w.n; c += 16) {
+        count += min(8, w.n - c);
+        if (!one) continue;
+        uint32_t r0[8], r1[8], r2[8], r3[8];
+        tmem_ld8(ta + c, r0);
+        tmem_ld8(ta + half + c, r1);
+        if (two) {
+          tmem_ld8(ta + C::TILE_COLS + c, r2);
+          tmem_ld8(ta + C::TILE_COLS + half + c, r3);
+        }
+        tmem_ld_wait();
+        float v0[8], v1[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v0[i] = __uint_as_float(r0[i]) + __uint_as_float(r1[i]);
+          v1[i] = two ? __uint_as_float(r2[i]) + __uint_as_float(r3[i]) : 0.f;
+        }
+        if (up) {
+          store_h_chunk(p.h, p.hs + ((size_t)w.tile * (f / 128) + row_a / 128) * C::SB_BYTES, f,
+                        w.row0, row_a + q * 32, c, w.n, half, q, lane, v0, v1);
+        } else {
+          float *y = p.b.y + (size_t)(w.row0 + c) * d + row_a + q * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float s = __shfl_sync(0xffffffffu, c >= 64 ? sc1 : sc0, ((c & 63) >> 4) * 8 + i);
+            if (c + i < w.n) {
+              y[(size_t)i * d] = v0[i] * s;
+              if (two) y[(size_t)i * d + 256] = v1[i] * s;
+            }
+          }
+        }
+      }
+      // every TMEM load has completed: the accumulator goes back before the stores drain
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_remote(tempty_leader);
+        __threadfence();
+        atomicAdd(up ? p.b.done + w.g : p.b.tile_done + w.mt, count);
+        if (up) atomicAdd(p.b.done_all, count);
+      }
+      __syncwarp();
+    }
+  }
+  if (alive && warp < kMxPairEpiWarps)
+    combine_pieces(p.b, p.b.slot_row, 512, n_rows * 8, warp, kMxPairEpiWarps, abort_flag);
+  // the pair leaves together: the leader's MMAs read the peer's shared memory, and the peer's
+  // copies signal the leader's barriers
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+  }
+}
+
+}  // namespace moe

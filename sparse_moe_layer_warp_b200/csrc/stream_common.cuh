@@ -74,19 +74,29 @@ __host__ __device__ __forceinline__ int token_tile_number(int off, int g, int i,
 
 // mbar_wait_bounded with long suspended tries: a dozen warps that poll would take the issue
 // slots of those that work.
+template <bool kCluster = false>
 __device__ __forceinline__ bool mbar_wait_suspend(uint64_t *bar, uint32_t parity,
                                                   volatile int *abort_flag, DevStatus *status,
                                                   int where,
                                                   unsigned long long limit_ns = kWaitLimitNs) {
   auto try_wait = [&]() {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)  // ns
-        : "memory");
+    if (kCluster)  // arrivals and data from the other CTA of a pair
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)  // ns
+          : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)  // ns
+          : "memory");
     return ok != 0;
   };
   if (try_wait()) return true;
@@ -244,24 +254,22 @@ __device__ __forceinline__ void build_tile_prefix(const StreamBase &p, const Str
   if (lane == 31) tb.tile_prefix[G] = incl;
 }
 
-// The scheduler: one thread claims units and hands them to the CTA's other roles through the
-// queue uq until none is left.
+// The scheduler: one thread claims units until none is left and hands each, the end (kind -1) last,
+// to publish(unit), which returns false when a wait gave up.  Scheduler `me` of n.
+template <typename Publish>
 __device__ __forceinline__ void schedule_units(const StreamBase &p, const StreamTables &tb, int bt,
-                                               int up_tiles, int down_tiles, Unit *uq,
-                                               uint64_t *uq_full, uint64_t *uq_empty,
-                                               volatile int *abort_flag) {
+                                               int up_tiles, int down_tiles, int me, int n,
+                                               Publish publish) {
   const int G = p.E + p.n_shared, n_tiles = tb.tile_prefix[G];
   const int n_up = n_tiles * up_tiles, n_units = n_up + n_tiles * down_tiles;
-  int qi = 0, pos = 0;  // pos: group (in group order) of the last unit
-  uint32_t qph = 0;
+  int pos = 0;  // group (in group order) of the last unit
   bool down = false;
   // tickets in hand, as the counter gave them (nothing is computed from a claim before its
   // turn: the thread would wait for the answer)
-  int t0 = (int)blockIdx.x - kClaimAhead * (int)gridDim.x, t1 = t0 + (int)gridDim.x,
-      t2 = t1 + (int)gridDim.x;
+  int t0 = me - kClaimAhead * n, t1 = t0 + n, t2 = t1 + n;
   static_assert(kClaimAhead == 3, "t0, t1, t2");
   while (true) {
-    int u = t0 + kClaimAhead * (int)gridDim.x;
+    int u = t0 + kClaimAhead * n;
     t0 = t1;
     t1 = t2;
     t2 = atomicAdd(p.sched, 1);
@@ -287,14 +295,7 @@ __device__ __forceinline__ void schedule_units(const StreamBase &p, const Stream
       r.row0 = off + r.tok0;
       r.tile = token_tile_number(off, r.g, r.tok0 / bt, bt);
     }
-    if (!mbar_wait_suspend(&uq_empty[qi], qph ^ 1, abort_flag, p.status, 31)) break;
-    uq[qi] = r;
-    mbar_arrive(&uq_full[qi]);
-    if (++qi == kUnitQ) {
-      qi = 0;
-      qph ^= 1;
-    }
-    if (r.kind < 0) break;
+    if (!publish(r) || r.kind < 0) break;
   }
 }
 

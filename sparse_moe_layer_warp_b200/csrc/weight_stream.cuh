@@ -282,7 +282,18 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   } else if (warp == kStreamWarps + 3) {
     // ---------------------------------------------------------------- scheduler
     if (lane == 0)
-      schedule_units(p.b, tb, BT, up_tiles, down_tiles, uq, uq_full, uq_empty, abort_flag);
+      schedule_units(p.b, tb, BT, up_tiles, down_tiles, blockIdx.x, gridDim.x,
+                     [&](const Unit &r) {
+                       if (!mbar_wait_suspend(&uq_empty[qi], qph ^ 1, abort_flag, p.b.status, 31))
+                         return false;
+                       uq[qi] = r;
+                       mbar_arrive(&uq_full[qi]);
+                       if (++qi == kUnitQ) {
+                         qi = 0;
+                         qph ^= 1;
+                       }
+                       return true;
+                     });
     __syncwarp();
   } else if (warp >= kStreamWarps + kStreamProdWarps) {
     // ---------------------------------------------------------------- epilogue

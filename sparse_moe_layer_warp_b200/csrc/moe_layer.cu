@@ -1652,14 +1652,18 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
                   split_rows(at<uint8_t>(ws, W.x_split), P, c.d_model),
                   at<uint8_t>(ws, W.x_scale))) != MOE_OK)
     return s;
-  return mx_token_tile(c, T) == 32 ? launch_mx<32, false>(L, x, T, out, ws, W, st)
-                                   : launch_mx_pair(L, x, T, out, ws, W, st);
+  if (mx_token_tile(c, T) != kMxPairBN) return launch_mx<32, false>(L, x, T, out, ws, W, st);
+  if ((s = launch_mx_pair(L, x, T, out, ws, W, st)) != MOE_OK) return s;
+  return launch(combine_kernel<__nv_bfloat16>,
+                dim3(grid_for((size_t)T * (c.d_model / 4), 256, L->num_sms)), dim3(256), 0, st,
+                (const float *)at<float>(ws, W.y), (const int *)at<int>(ws, W.slot_row), T,
+                c.top_k, T * c.top_k, c.n_shared, c.d_model, static_cast<__nv_bfloat16 *>(out));
 }
 
 int mxfp4_launches(const moe_layer *L, int T) {
   if (T == 0) return 0;
   if (few_shape(L->cfg, T)) return 1;
-  return (T <= kChunk ? 2 : 3) + 2;
+  return (T <= kChunk ? 2 : 3) + (mx_token_tile(L->cfg, T) == kMxPairBN ? 3 : 2);
 }
 }  // namespace
 

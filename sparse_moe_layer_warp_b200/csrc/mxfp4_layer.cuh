@@ -200,30 +200,34 @@ __device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[16]) {
 __device__ __forceinline__ void store_h_chunk(const SplitRows &h, uint8_t *hs, int f, int row0,
                                               int col, int c, int n, int lo0, int k, int lane,
                                               const float (&gate)[8], const float (&up)[8]) {
+  float v[8];
+  uint32_t s[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = swiglu(gate[j], up[j]);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    s[j] = act_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu));
+  uint8_t *to_hi = h.hi + (size_t)(row0 + c) * f + col + lane,
+          *to_lo = h.lo + (size_t)(row0 + c) * f + col + lane;
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
-    if (c + j >= n) break;
-    const float ha = swiglu(gate[j], up[j]), hb = swiglu(gate[j + 1], up[j + 1]);
-    const uint32_t sa =
-        act_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(ha) & 0x7fffffffu));
-    const uint32_t sb =
-        act_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(hb) & 0x7fffffffu));
     uint32_t hi, lo;
-    split_pair(ha, hb, sa, sb, hi, lo);
-    const size_t at = (size_t)(row0 + c + j) * f + col + lane;
-    h.hi[at] = (uint8_t)hi;
-    h.lo[at] = (uint8_t)lo;
-    const bool both = c + j + 1 < n;
-    if (both) {
-      h.hi[at + f] = (uint8_t)(hi >> 8);
-      h.lo[at + f] = (uint8_t)(lo >> 8);
-    }
-    if (lane < 4 && (both || lane < 2)) {  // lanes 0, 1: first token; 2, 3: second
-      const uint32_t s = lane < 2 ? sa : sb;
-      const int r = c + j + (lane >> 1);
-      hs[scale_row_at(lane & 1 ? lo0 + r : r) + k] = (uint8_t)(lane & 1 ? lo_scale_byte(s) : s);
-    }
+    split_pair(v[j], v[j + 1], s[j], s[j + 1], hi, lo);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (c + j + i < n) {
+        to_hi[(size_t)(j + i) * f] = (uint8_t)(hi >> (8 * i));
+        to_lo[(size_t)(j + i) * f] = (uint8_t)(lo >> (8 * i));
+      }
   }
+  // lane j writes token j's hi scale, lane 8 + j its lo scale
+  uint32_t mine = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if ((lane & 7) == j) mine = s[j];
+  const int r = c + (lane & 7);
+  if (lane < 16 && r < n)
+    hs[scale_row_at(lane < 8 ? r : lo0 + r) + k] = (uint8_t)(lane < 8 ? mine : lo_scale_byte(mine));
 }
 
 // x [T, d] -> the split rows of the sorted space with their scale blocks: token t to its k routed

@@ -8,10 +8,12 @@
 // each CTA holds and reads only half of the token rows -- the hi rows in the leader, the lo rows in
 // its peer.  A stage of 896 clocks then moves 106 KB: the tensor cores bind again.
 //
-// CTA r of a pair holds weight rows [128 r, 128 r + 128) of each 256-row tile; a unit has two tiles
-// (gate and up; two neighbours of W_d).  N follows the unit's tokens (2 x the next multiple of 8).
-// TMEM: 2 x 224 accumulator columns, so one unit at a time; two sets of scales.  The scales of all N
-// columns are needed by both CTAs, those of the weight rows by the CTA that holds them.
+// CTA r of a pair holds weight rows [128 r, 128 r + 128) of each 256-row tile; an up unit has two
+// tiles (gate and up), a down unit one.  N follows the unit's tokens (2 x the next multiple of 8).
+// TMEM: 2 x 224 accumulator columns -- an up unit takes both, down units take them in turn, so
+// that the stores of one run beside the products of the next -- and two sets of scales.  The scales
+// of all N columns are needed by both CTAs, those of the weight rows by the CTA that holds them.
+// The combine is a launch of its own: at these sizes y is larger than L2 and wants every warp.
 #pragma once
 #include "mxfp4_layer.cuh"
 
@@ -76,9 +78,9 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   uint8_t *sSB = sSA + S * C::SA_BYTES;     // [S][1024]
   uint64_t *full = reinterpret_cast<uint64_t *>(sSB + S * C::SB_BYTES);  // the leader's: both CTAs'
   uint64_t *empty = full + S;
-  uint64_t *tfull = empty + S;
-  uint64_t *tempty = tfull + 1;             // the leader's: both CTAs' epilogue warps
-  uint64_t *uq_full = tempty + 1;
+  uint64_t *tfull = empty + S;              // [2]
+  uint64_t *tempty = tfull + 2;             // [2], the leader's: both CTAs' epilogue warps
+  uint64_t *uq_full = tempty + 2;
   uint64_t *uq_empty = uq_full + kUnitQ;    // the leader's: both CTAs' readers
   uint64_t *mma_end = uq_empty + kUnitQ;
   Unit *uq = reinterpret_cast<Unit *>(mma_end + 1);
@@ -90,7 +92,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int Tk = p.b.T * p.b.k, d = p.b.d, f = p.b.f;
-  const int up_tiles = (f + 255) / 256, down_tiles = (d + 511) / 512;
+  const int up_tiles = (f + 255) / 256, down_tiles = (d + 255) / 256;
   const int n_rows = Tk + p.b.n_shared * p.b.T;
 
   if (threadIdx.x == 0) {
@@ -98,8 +100,10 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
       mbar_init(&full[s], 3);  // the leader's three producer warps
       mbar_init(&empty[s], 1);
     }
-    mbar_init(tfull, 1);
-    mbar_init(tempty, 2 * kMxPairEpiWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 2 * kMxPairEpiWarps);
+    }
     for (int q = 0; q < kUnitQ; ++q) {
       mbar_init(&uq_full[q], 1);
       mbar_init(&uq_empty[q], 2 * (kMxPairEpiWarps + 3) + 1);
@@ -142,10 +146,8 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     }
     return true;
   };
-  // first row (of the group's weights) of tile j of a unit in CTA r
-  auto tile_row = [&](const Unit &w, int j, int r) {
-    return w.kind == 0 ? w.mt * 256 + r * kMxTile : w.mt * 512 + j * 256 + r * kMxTile;
-  };
+  // first row (of the group's weights) of a unit's tile in CTA r
+  auto tile_row = [&](const Unit &w, int r) { return w.mt * 256 + r * kMxTile; };
   bool alive = true;
 
   if (warp == 12) {
@@ -171,7 +173,8 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
                      });
     __syncwarp();
   } else if (warp == 9 || warp == 10) {
-    // ---------------------------------------------------------------- weights (tile j)
+    // ---------------------------------------------------------------- weights
+    // Up: warp j loads gate or up rows with their scales.  Down: warp 0 the rows, warp 1 the scales.
     const int j = warp - 9;
     const uint64_t pol_once = policy_evict_first(), pol_reuse = policy_evict_last();
     int st = 0, filled = 0;
@@ -182,26 +185,25 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
       if (lane == 0) {
         const bool up = w.kind == 0;
         const int nk = (up ? d : f) / 128, m_rows = up ? f : d;
-        const bool there = tile_row(w, j, rank) < m_rows;
-        const int row = w.g * m_rows + tile_row(w, j, rank);
-        const uint32_t bytes = ((tile_row(w, j, 0) < m_rows) + (tile_row(w, j, 1) < m_rows)) *
-                               (kMxTile * 64 + kMxScaleBlock);  // of both CTAs
+        const bool there = tile_row(w, rank) < m_rows;
+        const int row = w.g * m_rows + tile_row(w, rank);
+        const bool codes = up || j == 0, scales = up || j == 1;
+        const uint32_t bytes = (1 + (tile_row(w, 1) < m_rows)) *  // of both CTAs
+                               ((codes ? kMxTile * 64 : 0) + (scales ? kMxScaleBlock : 0));
+        uint8_t *a = sA + (up ? j : 0) * (C::A_BYTES / 2);
+        uint8_t *sa = sSA + (up ? j : 0) * kMxScaleBlock;
         const CUtensorMap *m = up ? (j ? &p.tm_u : &p.tm_g) : &p.tm_d;
         const CUtensorMap *sc = up ? (j ? &p.tm_su : &p.tm_sg) : &p.tm_sd;
         const uint64_t pol = w.uses == 1 ? pol_once : pol_reuse;
         for (int kc = 0; kc < nk; ++kc) {
           ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 32);
           if (!ok) break;
-          if (leader) {
-            if (bytes) mbar_arrive_expect_tx(&full[st], bytes);
-            else mbar_arrive(&full[st]);
-          }
+          if (leader) mbar_arrive_expect_tx(&full[st], bytes);
           if (there) {
             const uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
-            tma_load_2d_pair(sA + st * C::A_BYTES + j * (C::A_BYTES / 2), m, bar, kc * 128, row,
-                             pol);
-            tma_load_2d_pair(sSA + st * C::SA_BYTES + j * kMxScaleBlock, sc, bar, 0,
-                             row / kMxTile * nk + kc, pol);
+            if (codes) tma_load_2d_pair(a + st * C::A_BYTES, m, bar, kc * 128, row, pol);
+            if (scales)
+              tma_load_2d_pair(sa + st * C::SA_BYTES, sc, bar, 0, row / kMxTile * nk + kc, pol);
           }
           ++filled;
           if (++st == S) {
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   } else if (warp == 8) {
     // ---------------------------------------------------------------- MMA (leader)
     if (leader) {
-      int st = 0, it = 0;
+      int st = 0, n0 = 0, n1 = 0, a0 = 0;  // uses of the accumulators; next down unit's
       uint32_t ph = 0;
       Unit w;
       const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem_base);
@@ -270,9 +272,12 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         if (kind < 0) break;
         const int nk = (kind == 0 ? d : f) / 128;
         const int half = scale_lo_row(__reduce_max_sync(0xffffffffu, w.n), BN);
-        const bool two = kind == 0 || __reduce_max_sync(0xffffffffu, w.mt) * 512 + 256 < d;
-        bool ok = warp_wait(tempty, (it & 1) ^ 1, 46);
-        ++it;
+        const bool two = kind == 0, use0 = two || a0 == 0, use1 = two || a0 == 1;
+        bool ok = true;
+        if (use0) ok = warp_wait(&tempty[0], (n0++ & 1) ^ 1, 46);
+        if (ok && use1) ok = warp_wait(&tempty[1], (n1++ & 1) ^ 1, 46);
+        const uint32_t d0 = tm + (use0 ? 0 : C::TILE_COLS);
+        if (!two) a0 ^= 1;
         tc_fence_after();
         for (int kc = 0; ok && kc < nk; ++kc) {
           ok = warp_wait(&full[st], ph, 37);
@@ -293,12 +298,13 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
             for (int kk = 0; kk < 4; ++kk) {
               const uint32_t id = id0 | ((uint32_t)kk << 4) | ((uint32_t)kk << 29);
               const uint32_t add = (kc | kk) ? 1u : 0u;
-              tc_mma_mx_pair(tm, a + 2 * kk, b + 2 * kk, id, sf, sf + 8, add);
+              tc_mma_mx_pair(d0, a + 2 * kk, b + 2 * kk, id, sf, sf + 8, add);
               if (two) tc_mma_mx_pair(tm + C::TILE_COLS, a2 + 2 * kk, b + 2 * kk, id, sf + 4,
                                       sf + 8, add);
             }
             tc_commit_pair_both(&empty[st]);
-            if (kc == nk - 1) tc_commit_pair_both(tfull);
+            if (kc == nk - 1 && use0) tc_commit_pair_both(&tfull[0]);
+            if (kc == nk - 1 && use1) tc_commit_pair_both(&tfull[1]);
           }
           __syncwarp();
           if (++st == S) {
@@ -320,13 +326,14 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     // Chunks of 8 tokens, alternating between the two warps of a quadrant.
     const int q = warp & 3, eh = warp >> 2;
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
-    int it = 0;
+    int n0 = 0, n1 = 0, a0 = 0;
     Unit w;
     while ((alive = next_unit(w, 42)) && w.kind >= 0) {
       const bool up = w.kind == 0;
       const int m_rows = up ? f : d, half = scale_lo_row(w.n, BN);
-      const int row_a = tile_row(w, 0, rank), row_b = tile_row(w, 1, rank);
-      const bool one = row_a < m_rows, two = row_b < m_rows;
+      const int row_a = tile_row(w, rank);
+      const bool there = row_a < m_rows, use0 = up || a0 == 0, use1 = up || a0 == 1;
+      if (!up) a0 ^= 1;
       // down: routed_scale * gate of this warp's tokens (lane, lane + 32), asked for before the wait
       float sc0 = 1.f, sc1 = 1.f;
       if (!up && w.g < p.b.E) {
@@ -334,19 +341,19 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         if (i0 < w.n) sc0 = p.b.routed_scale * p.b.gate[p.b.perm[w.row0 + i0]];
         if (i1 < w.n) sc1 = p.b.routed_scale * p.b.gate[p.b.perm[w.row0 + i1]];
       }
-      alive = warp_wait(tfull, it & 1, 39);
+      if (use0) alive = warp_wait(&tfull[0], n0++ & 1, 39);
+      if (alive && use1) alive = warp_wait(&tfull[1], n1++ & 1, 39);
       if (!alive) break;
-      ++it;
       tc_fence_after();
-      const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16);
+      const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + (use0 ? 0 : C::TILE_COLS);
       int count = 0;
       for (int c = 8 * eh; c < w.n; c += 16) {
         count += min(8, w.n - c);
-        if (!one) continue;
+        if (!there) continue;
         uint32_t r0[8], r1[8], r2[8], r3[8];
         tmem_ld8(ta + c, r0);
         tmem_ld8(ta + half + c, r1);
-        if (two) {
+        if (up) {
           tmem_ld8(ta + C::TILE_COLS + c, r2);
           tmem_ld8(ta + C::TILE_COLS + half + c, r3);
         }
@@ -355,7 +362,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           v0[i] = __uint_as_float(r0[i]) + __uint_as_float(r1[i]);
-          v1[i] = two ? __uint_as_float(r2[i]) + __uint_as_float(r3[i]) : 0.f;
+          v1[i] = up ? __uint_as_float(r2[i]) + __uint_as_float(r3[i]) : 0.f;
         }
         if (up) {
           store_h_chunk(p.h, p.hs + ((size_t)w.tile * (f / 128) + row_a / 128) * C::SB_BYTES, f,
@@ -365,10 +372,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float s = __shfl_sync(0xffffffffu, c >= 64 ? sc1 : sc0, ((c & 63) >> 4) * 8 + i);
-            if (c + i < w.n) {
-              y[(size_t)i * d] = v0[i] * s;
-              if (two) y[(size_t)i * d + 256] = v1[i] * s;
-            }
+            if (c + i < w.n) y[(size_t)i * d] = v0[i] * s;
           }
         }
       }
@@ -376,16 +380,17 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_remote(tempty_leader);
-        __threadfence();
-        atomicAdd(up ? p.b.done + w.g : p.b.tile_done + w.mt, count);
-        if (up) atomicAdd(p.b.done_all, count);
+        if (use0) mbar_arrive_remote(tempty_leader);
+        if (use1) mbar_arrive_remote(tempty_leader + 8);
+        if (up) {
+          __threadfence();
+          atomicAdd(p.b.done + w.g, count);
+          atomicAdd(p.b.done_all, count);
+        }
       }
       __syncwarp();
     }
   }
-  if (alive && warp < kMxPairEpiWarps)
-    combine_pieces(p.b, p.b.slot_row, 512, n_rows * 8, warp, kMxPairEpiWarps, abort_flag);
   // the pair leaves together: the leader's MMAs read the peer's shared memory, and the peer's
   // copies signal the leader's barriers
   tc_fence_before();

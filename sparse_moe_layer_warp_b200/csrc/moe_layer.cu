@@ -1654,10 +1654,11 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
     return s;
   if (mx_token_tile(c, T) != kMxPairBN) return launch_mx<32, false>(L, x, T, out, ws, W, st);
   if ((s = launch_mx_pair(L, x, T, out, ws, W, st)) != MOE_OK) return s;
-  return launch(combine_kernel<__nv_bfloat16>,
+  return launch(mxfp4_combine_kernel,
                 dim3(grid_for((size_t)T * (c.d_model / 4), 256, L->num_sms)), dim3(256), 0, st,
-                (const float *)at<float>(ws, W.y), (const int *)at<int>(ws, W.slot_row), T,
-                c.top_k, T * c.top_k, c.n_shared, c.d_model, static_cast<__nv_bfloat16 *>(out));
+                (const float *)at<float>(ws, W.y), (const int *)at<int>(ws, W.slot_row),
+                (const float *)at<float>(ws, W.gate), c.routed_scale, T, c.top_k, c.n_shared,
+                c.d_model, static_cast<__nv_bfloat16 *>(out));
 }
 
 int mxfp4_launches(const moe_layer *L, int T) {

@@ -194,40 +194,55 @@ __device__ __forceinline__ void load16(const __nv_bfloat16 *p, float (&v)[16]) {
   }
 }
 
-// Eight tokens (c .. c + 7 of a tile of n) x a warp's 32 columns of h, from the sums of gate and up,
-// as split values with the scale byte k of their rows: col the first column, hs the tile's scale
-// block of these 128 columns, lo0 the block's first lo row.
+// 8 x 8 bytes across 8 neighbouring lanes: byte j of lane i (a: bytes 0-3, b: 4-7) becomes byte i of
+// lane j.  Three exchanges of 32 bits.
+__device__ __forceinline__ void transpose_bytes(uint32_t &a, uint32_t &b, int lane) {
+  const bool u4 = lane & 4, u2 = lane & 2, u1 = lane & 1;
+  uint32_t t = __shfl_xor_sync(0xffffffffu, u4 ? a : b, 4);
+  if (u4) a = t;
+  else b = t;
+  // halves: lanes with bit 1 clear keep the low ones
+  t = __shfl_xor_sync(0xffffffffu, __byte_perm(a, b, u2 ? 0x5410 : 0x7632), 2);
+  a = __byte_perm(a, t, u2 ? 0x3254 : 0x5410);
+  b = __byte_perm(b, t, u2 ? 0x3276 : 0x7610);
+  // bytes: lanes with bit 0 clear keep bytes 0 and 2
+  t = __shfl_xor_sync(0xffffffffu, __byte_perm(a, b, u1 ? 0x6420 : 0x7531), 1);
+  a = __byte_perm(a, t, u1 ? 0x3514 : 0x5240);
+  b = __byte_perm(b, t, u1 ? 0x3716 : 0x7260);
+}
+
+// Eight tokens (c .. c + 7 of a tile of n) x a warp's 32 columns of h (lane: column) as split values
+// with the scale byte k of their rows: col the first column, hs the tile's scale block of these 128
+// columns, lo0 the block's first lo row.  The bytes are transposed so that a lane stores 8
+// neighbours of one token: as 16 one-byte stores a lane they took half of the up epilogue.
 __device__ __forceinline__ void store_h_chunk(const SplitRows &h, uint8_t *hs, int f, int row0,
                                               int col, int c, int n, int lo0, int k, int lane,
-                                              const float (&gate)[8], const float (&up)[8]) {
-  float v[8];
-  uint32_t s[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = swiglu(gate[j], up[j]);
+                                              const float (&v)[8]) {
+  uint32_t s[8], hi[4], lo[4];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     s[j] = act_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu));
-  uint8_t *to_hi = h.hi + (size_t)(row0 + c) * f + col + lane,
-          *to_lo = h.lo + (size_t)(row0 + c) * f + col + lane;
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    uint32_t hi, lo;
-    split_pair(v[j], v[j + 1], s[j], s[j + 1], hi, lo);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (c + j + i < n) {
-        to_hi[(size_t)(j + i) * f] = (uint8_t)(hi >> (8 * i));
-        to_lo[(size_t)(j + i) * f] = (uint8_t)(lo >> (8 * i));
-      }
-  }
-  // lane j writes token j's hi scale, lane 8 + j its lo scale
+  for (int j = 0; j < 4; ++j)
+    split_pair(v[2 * j], v[2 * j + 1], s[2 * j], s[2 * j + 1], hi[j], lo[j]);
+  uint32_t hi_a = hi[0] | hi[1] << 16, hi_b = hi[2] | hi[3] << 16;
+  uint32_t lo_a = lo[0] | lo[1] << 16, lo_b = lo[2] | lo[3] << 16;
+  transpose_bytes(hi_a, hi_b, lane);
+  transpose_bytes(lo_a, lo_b, lane);
+  // lanes t, 8 + t, 16 + t, 24 + t: token t.  Lane t also writes its hi scale, lane 8 + t its lo
+  const int t = lane & 7, r = c + t;
   uint32_t mine = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if ((lane & 7) == j) mine = s[j];
-  const int r = c + (lane & 7);
-  if (lane < 16 && r < n)
-    hs[scale_row_at(lane < 8 ? r : lo0 + r) + k] = (uint8_t)(lane < 8 ? mine : lo_scale_byte(mine));
+    if (t == j) mine = s[j];
+  if (r < n) {
+    const size_t at = (size_t)(row0 + r) * f + col + (lane & 24);
+    *reinterpret_cast<uint2 *>(h.hi + at) = make_uint2(hi_a, hi_b);
+    *reinterpret_cast<uint2 *>(h.lo + at) = make_uint2(lo_a, lo_b);
+    if (lane < 16)
+      hs[scale_row_at(lane < 8 ? r : lo0 + r) + k] =
+          (uint8_t)(lane < 8 ? mine : lo_scale_byte(mine));
+  }
 }
 
 // x [T, d] -> the split rows of the sorted space with their scale blocks: token t to its k routed
@@ -657,8 +672,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           v1[j] = two ? __uint_as_float(r2[j]) + __uint_as_float(r3[j]) : 0.f;
         }
         if (up) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v0[j] = swiglu(v0[j], v1[j]);
           store_h_chunk(p.h, p.hs + ((size_t)w.tile * (f / 128) + w.mt) * C::SB_BYTES, f, w.row0,
-                        w.mt * kMxTile + warp * 32, c, w.n, BN, warp, lane, v0, v1);
+                        w.mt * kMxTile + warp * 32, c, w.n, BN, warp, lane, v0);
         } else {
           float *y = p.b.y + (size_t)(w.row0 + c) * d + w.mt * kMxDown + warp * 32 + lane;
 #pragma unroll

@@ -20,7 +20,7 @@
 namespace moe {
 
 constexpr int kMxPairEpiWarps = 8;  // warps 0-7: two for each TMEM lane quadrant
-constexpr int kMxPairThreads = 32 * 16;  // 8 MMA, 9-10 weights, 11 token rows, 12 scheduler
+constexpr int kMxPairThreads = 32 * 13;  // 8 MMA, 9-10 weights, 11 token rows, 12 scheduler
 
 struct MxPairParams {
   StreamBase b;
@@ -323,7 +323,11 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     __syncwarp();
   } else if (warp < kMxPairEpiWarps) {
     // ---------------------------------------------------------------- epilogue
-    // Chunks of 8 tokens, alternating between the two warps of a quadrant.
+    // Chunks of 8 tokens, alternating between the two warps of a quadrant.  All of a unit's values
+    // are read before the first is stored: the accumulator goes back some thousand clocks earlier
+    // (the release of the arrival would also wait for the stores).  y is left without the gates,
+    // which the combine applies: looking them up cost two dependent loads a unit here.
+    constexpr int CH = BN / 16;
     const int q = warp & 3, eh = warp >> 2;
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
     int n0 = 0, n1 = 0, a0 = 0;
@@ -334,22 +338,16 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
       const int row_a = tile_row(w, rank);
       const bool there = row_a < m_rows, use0 = up || a0 == 0, use1 = up || a0 == 1;
       if (!up) a0 ^= 1;
-      // down: routed_scale * gate of this warp's tokens (lane, lane + 32), asked for before the wait
-      float sc0 = 1.f, sc1 = 1.f;
-      if (!up && w.g < p.b.E) {
-        const int i0 = (lane >> 3) * 16 + eh * 8 + (lane & 7), i1 = i0 + 64;
-        if (i0 < w.n) sc0 = p.b.routed_scale * p.b.gate[p.b.perm[w.row0 + i0]];
-        if (i1 < w.n) sc1 = p.b.routed_scale * p.b.gate[p.b.perm[w.row0 + i1]];
-      }
       if (use0) alive = warp_wait(&tfull[0], n0++ & 1, 39);
       if (alive && use1) alive = warp_wait(&tfull[1], n1++ & 1, 39);
       if (!alive) break;
       tc_fence_after();
       const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + (use0 ? 0 : C::TILE_COLS);
-      int count = 0;
-      for (int c = 8 * eh; c < w.n; c += 16) {
-        count += min(8, w.n - c);
-        if (!there) continue;
+      float v[CH][8];
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = 16 * i + 8 * eh;
+        if (c >= w.n || !there) continue;
         uint32_t r0[8], r1[8], r2[8], r3[8];
         tmem_ld8(ta + c, r0);
         tmem_ld8(ta + half + c, r1);
@@ -358,35 +356,40 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
           tmem_ld8(ta + C::TILE_COLS + half + c, r3);
         }
         tmem_ld_wait();
-        float v0[8], v1[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v0[i] = __uint_as_float(r0[i]) + __uint_as_float(r1[i]);
-          v1[i] = up ? __uint_as_float(r2[i]) + __uint_as_float(r3[i]) : 0.f;
-        }
-        if (up) {
-          store_h_chunk(p.h, p.hs + ((size_t)w.tile * (f / 128) + row_a / 128) * C::SB_BYTES, f,
-                        w.row0, row_a + q * 32, c, w.n, half, q, lane, v0, v1);
-        } else {
-          float *y = p.b.y + (size_t)(w.row0 + c) * d + row_a + q * 32 + lane;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float s = __shfl_sync(0xffffffffu, c >= 64 ? sc1 : sc0, ((c & 63) >> 4) * 8 + i);
-            if (c + i < w.n) y[(size_t)i * d] = v0[i] * s;
-          }
+        for (int j = 0; j < 8; ++j) {
+          v[i][j] = __uint_as_float(r0[j]) + __uint_as_float(r1[j]);
+          if (up) v[i][j] = swiglu(v[i][j], __uint_as_float(r2[j]) + __uint_as_float(r3[j]));
         }
       }
-      // every TMEM load has completed: the accumulator goes back before the stores drain
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (use0) mbar_arrive_remote(tempty_leader);
         if (use1) mbar_arrive_remote(tempty_leader + 8);
+      }
+      int count = 0;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int c = 16 * i + 8 * eh;
+        if (c >= w.n) continue;
+        count += min(8, w.n - c);
+        if (!there) continue;
         if (up) {
-          __threadfence();
-          atomicAdd(p.b.done + w.g, count);
-          atomicAdd(p.b.done_all, count);
+          store_h_chunk(p.h, p.hs + ((size_t)w.tile * (f / 128) + row_a / 128) * C::SB_BYTES, f,
+                        w.row0, row_a + q * 32, c, w.n, half, q, lane, v[i]);
+        } else {
+          float *y = p.b.y + (size_t)(w.row0 + c) * d + row_a + q * 32 + lane;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (c + j < w.n) y[(size_t)j * d] = v[i][j];
         }
+      }
+      __syncwarp();
+      if (up && lane == 0) {
+        __threadfence();
+        atomicAdd(p.b.done + w.g, count);
+        atomicAdd(p.b.done_all, count);
       }
       __syncwarp();
     }
@@ -399,6 +402,50 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// out[t] = sum_j routed_scale * gate[t, j] * y[slot_row[t, j]] + y[shared row t], in this order in
+// fp32, one rounding.  Four columns a thread; bound by HBM (y is read once).
+__global__ void __launch_bounds__(256)
+    mxfp4_combine_kernel(const float *__restrict__ y, const int *__restrict__ slot_row,
+                         const float *__restrict__ gate, float routed_scale, int T, int k,
+                         int n_shared, int d, __nv_bfloat16 *__restrict__ out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int vpr = d / 4;
+  const size_t n = (size_t)T * vpr, step = (size_t)gridDim.x * blockDim.x;
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
+    const size_t t = i / vpr, c = i % vpr * 4;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < k; j0 += 8) {  // eight rows in flight, added in slot order
+      float g[8];
+      float4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = j0 + j < k;
+        g[j] = in ? routed_scale * __ldg(gate + t * k + j0 + j) : 0.f;
+        v[j] = in ? __ldg(reinterpret_cast<const float4 *>(
+                        y + (size_t)__ldg(slot_row + t * k + j0 + j) * d + c))
+                  : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < k) {
+          s.x = fmaf(g[j], v[j].x, s.x);
+          s.y = fmaf(g[j], v[j].y, s.y);
+          s.z = fmaf(g[j], v[j].z, s.z);
+          s.w = fmaf(g[j], v[j].w, s.w);
+        }
+    }
+    if (n_shared) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(y + ((size_t)T * k + t) * d + c));
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
+    store4(out + t * d + c, s);
   }
 }
 

@@ -8,19 +8,19 @@
 // each CTA holds and reads only half of the token rows -- the hi rows in the leader, the lo rows in
 // its peer.  A stage of 896 clocks then moves 106 KB: the tensor cores bind again.
 //
-// CTA r of a pair holds weight rows [128 r, 128 r + 128) of each 256-row tile; an up unit has two
-// tiles (gate and up), a down unit one.  N follows the unit's tokens (2 x the next multiple of 8).
-// TMEM: 2 x 224 accumulator columns -- an up unit takes both, down units take them in turn, so
-// that the stores of one run beside the products of the next -- and two sets of scales.  The scales
-// of all N columns are needed by both CTAs, those of the weight rows by the CTA that holds them.
+// CTA r of a pair holds weight rows [128 r, 128 r + 128) of each 256-row tile; a unit has two tiles
+// (gate and up; two neighbours of W_d).  N follows the unit's tokens (2 x the next multiple of 8).
+// TMEM: 2 x 224 accumulator columns, so one unit at a time, and two sets of scales.  The scales of
+// all N columns are needed by both CTAs, those of the weight rows by the CTA that holds them.
 // The combine is a launch of its own: at these sizes y is larger than L2 and wants every warp.
 #pragma once
 #include "mxfp4_layer.cuh"
 
 namespace moe {
 
-constexpr int kMxPairEpiWarps = 8;  // warps 0-7: two for each TMEM lane quadrant
-constexpr int kMxPairThreads = 32 * 13;  // 8 MMA, 9-10 weights, 11 token rows, 12 scheduler
+constexpr int kMxPairEpiWarps = 16;  // warps 0-15: four for each TMEM lane quadrant
+// then MMA, two warps for the weights, token rows, scheduler
+constexpr int kMxPairThreads = 32 * (kMxPairEpiWarps + 5);
 
 struct MxPairParams {
   StreamBase b;
@@ -78,9 +78,9 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   uint8_t *sSB = sSA + S * C::SA_BYTES;     // [S][1024]
   uint64_t *full = reinterpret_cast<uint64_t *>(sSB + S * C::SB_BYTES);  // the leader's: both CTAs'
   uint64_t *empty = full + S;
-  uint64_t *tfull = empty + S;              // [2]
-  uint64_t *tempty = tfull + 2;             // [2], the leader's: both CTAs' epilogue warps
-  uint64_t *uq_full = tempty + 2;
+  uint64_t *tfull = empty + S;
+  uint64_t *tempty = tfull + 1;             // the leader's: both CTAs' epilogue warps
+  uint64_t *uq_full = tempty + 1;
   uint64_t *uq_empty = uq_full + kUnitQ;    // the leader's: both CTAs' readers
   uint64_t *mma_end = uq_empty + kUnitQ;
   Unit *uq = reinterpret_cast<Unit *>(mma_end + 1);
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int Tk = p.b.T * p.b.k, d = p.b.d, f = p.b.f;
-  const int up_tiles = (f + 255) / 256, down_tiles = (d + 255) / 256;
+  const int up_tiles = (f + 255) / 256, down_tiles = (d + 511) / 512;
   const int n_rows = Tk + p.b.n_shared * p.b.T;
 
   if (threadIdx.x == 0) {
@@ -100,10 +100,8 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
       mbar_init(&full[s], 3);  // the leader's three producer warps
       mbar_init(&empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 2 * kMxPairEpiWarps);
-    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, 2 * kMxPairEpiWarps);
     for (int q = 0; q < kUnitQ; ++q) {
       mbar_init(&uq_full[q], 1);
       mbar_init(&uq_empty[q], 2 * (kMxPairEpiWarps + 3) + 1);
@@ -115,7 +113,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     tma_prefetch_desc(&p.tm_u);
     tma_prefetch_desc(&p.tm_d);
   }
-  if (warp == 8) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+  if (warp == kMxPairEpiWarps) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
   griddep_wait();
   griddep_launch_dependents();
   for (int e = threadIdx.x; e <= p.b.E; e += blockDim.x) tb.offsets[e] = p.b.offsets[e];
@@ -146,11 +144,13 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     }
     return true;
   };
-  // first row (of the group's weights) of a unit's tile in CTA r
-  auto tile_row = [&](const Unit &w, int r) { return w.mt * 256 + r * kMxTile; };
+  // first row (of the group's weights) of tile j of a unit in CTA r
+  auto tile_row = [&](const Unit &w, int j, int r) {
+    return w.kind == 0 ? w.mt * 256 + r * kMxTile : w.mt * 512 + j * 256 + r * kMxTile;
+  };
   bool alive = true;
 
-  if (warp == 12) {
+  if (warp == kMxPairEpiWarps + 4) {
     if (lane == 0 && leader)
       schedule_units(p.b, tb, BN, up_tiles, down_tiles, blockIdx.x >> 1, gridDim.x >> 1,
                      [&](const Unit &r) {
@@ -172,10 +172,10 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
                        return true;
                      });
     __syncwarp();
-  } else if (warp == 9 || warp == 10) {
+  } else if (warp == kMxPairEpiWarps + 1 || warp == kMxPairEpiWarps + 2) {
     // ---------------------------------------------------------------- weights
-    // Up: warp j loads gate or up rows with their scales.  Down: warp 0 the rows, warp 1 the scales.
-    const int j = warp - 9;
+    // Warp j: tile j of the unit.
+    const int j = warp - (kMxPairEpiWarps + 1);
     const uint64_t pol_once = policy_evict_first(), pol_reuse = policy_evict_last();
     int st = 0, filled = 0;
     uint32_t ph = 0;
@@ -185,25 +185,25 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
       if (lane == 0) {
         const bool up = w.kind == 0;
         const int nk = (up ? d : f) / 128, m_rows = up ? f : d;
-        const bool there = tile_row(w, rank) < m_rows;
-        const int row = w.g * m_rows + tile_row(w, rank);
-        const bool codes = up || j == 0, scales = up || j == 1;
-        const uint32_t bytes = (1 + (tile_row(w, 1) < m_rows)) *  // of both CTAs
-                               ((codes ? kMxTile * 64 : 0) + (scales ? kMxScaleBlock : 0));
-        uint8_t *a = sA + (up ? j : 0) * (C::A_BYTES / 2);
-        uint8_t *sa = sSA + (up ? j : 0) * kMxScaleBlock;
+        const bool there = tile_row(w, j, rank) < m_rows;
+        const int row = w.g * m_rows + tile_row(w, j, rank);
+        const uint32_t bytes = ((tile_row(w, j, 0) < m_rows) + (tile_row(w, j, 1) < m_rows)) *
+                               (kMxTile * 64 + kMxScaleBlock);  // of both CTAs
+        uint8_t *a = sA + j * (C::A_BYTES / 2), *sa = sSA + j * kMxScaleBlock;
         const CUtensorMap *m = up ? (j ? &p.tm_u : &p.tm_g) : &p.tm_d;
         const CUtensorMap *sc = up ? (j ? &p.tm_su : &p.tm_sg) : &p.tm_sd;
         const uint64_t pol = w.uses == 1 ? pol_once : pol_reuse;
         for (int kc = 0; kc < nk; ++kc) {
           ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 32);
           if (!ok) break;
-          if (leader) mbar_arrive_expect_tx(&full[st], bytes);
+          if (leader) {
+            if (bytes) mbar_arrive_expect_tx(&full[st], bytes);
+            else mbar_arrive(&full[st]);
+          }
           if (there) {
             const uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
-            if (codes) tma_load_2d_pair(a + st * C::A_BYTES, m, bar, kc * 128, row, pol);
-            if (scales)
-              tma_load_2d_pair(sa + st * C::SA_BYTES, sc, bar, 0, row / kMxTile * nk + kc, pol);
+            tma_load_2d_pair(a + st * C::A_BYTES, m, bar, kc * 128, row, pol);
+            tma_load_2d_pair(sa + st * C::SA_BYTES, sc, bar, 0, row / kMxTile * nk + kc, pol);
           }
           ++filled;
           if (++st == S) {
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     }
     if (!ok && lane == 0 && leader) drain_stages(full, filled, S);
     __syncwarp();
-  } else if (warp == 11) {
+  } else if (warp == kMxPairEpiWarps + 3) {
     // ---------------------------------------------------------------- token rows
     const int h_target = n_rows * up_tiles * 8;
     const uint64_t pol = policy_evict_last();
@@ -258,10 +258,10 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     }
     if (!ok && lane == 0 && leader) drain_stages(full, filled, S);
     __syncwarp();
-  } else if (warp == 8) {
+  } else if (warp == kMxPairEpiWarps) {
     // ---------------------------------------------------------------- MMA (leader)
     if (leader) {
-      int st = 0, n0 = 0, n1 = 0, a0 = 0;  // uses of the accumulators; next down unit's
+      int st = 0, it = 0;
       uint32_t ph = 0;
       Unit w;
       const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem_base);
@@ -272,12 +272,9 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         if (kind < 0) break;
         const int nk = (kind == 0 ? d : f) / 128;
         const int half = scale_lo_row(__reduce_max_sync(0xffffffffu, w.n), BN);
-        const bool two = kind == 0, use0 = two || a0 == 0, use1 = two || a0 == 1;
-        bool ok = true;
-        if (use0) ok = warp_wait(&tempty[0], (n0++ & 1) ^ 1, 46);
-        if (ok && use1) ok = warp_wait(&tempty[1], (n1++ & 1) ^ 1, 46);
-        const uint32_t d0 = tm + (use0 ? 0 : C::TILE_COLS);
-        if (!two) a0 ^= 1;
+        const bool two = kind == 0 || __reduce_max_sync(0xffffffffu, w.mt) * 512 + 256 < d;
+        bool ok = warp_wait(tempty, (it & 1) ^ 1, 46);
+        ++it;
         tc_fence_after();
         for (int kc = 0; ok && kc < nk; ++kc) {
           ok = warp_wait(&full[st], ph, 37);
@@ -298,13 +295,12 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
             for (int kk = 0; kk < 4; ++kk) {
               const uint32_t id = id0 | ((uint32_t)kk << 4) | ((uint32_t)kk << 29);
               const uint32_t add = (kc | kk) ? 1u : 0u;
-              tc_mma_mx_pair(d0, a + 2 * kk, b + 2 * kk, id, sf, sf + 8, add);
+              tc_mma_mx_pair(tm, a + 2 * kk, b + 2 * kk, id, sf, sf + 8, add);
               if (two) tc_mma_mx_pair(tm + C::TILE_COLS, a2 + 2 * kk, b + 2 * kk, id, sf + 4,
                                       sf + 8, add);
             }
             tc_commit_pair_both(&empty[st]);
-            if (kc == nk - 1 && use0) tc_commit_pair_both(&tfull[0]);
-            if (kc == nk - 1 && use1) tc_commit_pair_both(&tfull[1]);
+            if (kc == nk - 1) tc_commit_pair_both(tfull);
           }
           __syncwarp();
           if (++st == S) {
@@ -323,66 +319,66 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     __syncwarp();
   } else if (warp < kMxPairEpiWarps) {
     // ---------------------------------------------------------------- epilogue
-    // Chunks of 8 tokens, alternating between the two warps of a quadrant.  All of a unit's values
-    // are read before the first is stored: the accumulator goes back some thousand clocks earlier
-    // (the release of the arrival would also wait for the stores).  y is left without the gates,
-    // which the combine applies: looking them up cost two dependent loads a unit here.
-    constexpr int CH = BN / 16;
-    const int q = warp & 3, eh = warp >> 2;
+    // Chunks of 8 tokens, dealt to the four warps of a quadrant.  All of a unit's values are read
+    // before the first is stored, and the accumulator goes back at once.  y is left without the
+    // gates, which the combine applies: looking them up cost two dependent loads a unit here.
+    constexpr int CH = (BN / 8 + 3) / 4;
+    const int q = warp & 3, c0 = warp >> 2 << 3;
     const uint32_t tempty_leader = mapa_shared(smem_u32(tempty), 0);
-    int n0 = 0, n1 = 0, a0 = 0;
+    int it = 0;
     Unit w;
     while ((alive = next_unit(w, 42)) && w.kind >= 0) {
       const bool up = w.kind == 0;
       const int m_rows = up ? f : d, half = scale_lo_row(w.n, BN);
-      const int row_a = tile_row(w, rank);
-      const bool there = row_a < m_rows, use0 = up || a0 == 0, use1 = up || a0 == 1;
-      if (!up) a0 ^= 1;
-      if (use0) alive = warp_wait(&tfull[0], n0++ & 1, 39);
-      if (alive && use1) alive = warp_wait(&tfull[1], n1++ & 1, 39);
+      const int row_a = tile_row(w, 0, rank), row_b = tile_row(w, 1, rank);
+      const bool one = row_a < m_rows, two = row_b < m_rows;
+      alive = warp_wait(tfull, it & 1, 39);
       if (!alive) break;
+      ++it;
       tc_fence_after();
-      const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + (use0 ? 0 : C::TILE_COLS);
-      float v[CH][8];
+      const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16);
+      float v0[CH][8], v1[CH][8];
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = 16 * i + 8 * eh;
-        if (c >= w.n || !there) continue;
-        uint32_t r0[8], r1[8], r2[8], r3[8];
+        const int c = 32 * i + c0;
+        if (c >= w.n || !one) continue;
+        uint32_t r0[8], r1[8];
         tmem_ld8(ta + c, r0);
         tmem_ld8(ta + half + c, r1);
-        if (up) {
-          tmem_ld8(ta + C::TILE_COLS + c, r2);
-          tmem_ld8(ta + C::TILE_COLS + half + c, r3);
-        }
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          v[i][j] = __uint_as_float(r0[j]) + __uint_as_float(r1[j]);
-          if (up) v[i][j] = swiglu(v[i][j], __uint_as_float(r2[j]) + __uint_as_float(r3[j]));
-        }
+        for (int j = 0; j < 8; ++j) v0[i][j] = __uint_as_float(r0[j]) + __uint_as_float(r1[j]);
+        if (!two) continue;
+        tmem_ld8(ta + C::TILE_COLS + c, r0);
+        tmem_ld8(ta + C::TILE_COLS + half + c, r1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v1[i][j] = __uint_as_float(r0[j]) + __uint_as_float(r1[j]);
       }
+      // the loads have completed (tcgen05.wait::ld); nothing else is handed over
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (use0) mbar_arrive_remote(tempty_leader);
-        if (use1) mbar_arrive_remote(tempty_leader + 8);
-      }
+      if (lane == 0) mbar_arrive_remote_relaxed(tempty_leader);
       int count = 0;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int c = 16 * i + 8 * eh;
+        const int c = 32 * i + c0;
         if (c >= w.n) continue;
         count += min(8, w.n - c);
-        if (!there) continue;
+        if (!one) continue;
         if (up) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v0[i][j] = swiglu(v0[i][j], v1[i][j]);
           store_h_chunk(p.h, p.hs + ((size_t)w.tile * (f / 128) + row_a / 128) * C::SB_BYTES, f,
-                        w.row0, row_a + q * 32, c, w.n, half, q, lane, v[i]);
+                        w.row0, row_a + q * 32, c, w.n, half, q, lane, v0[i]);
         } else {
           float *y = p.b.y + (size_t)(w.row0 + c) * d + row_a + q * 32 + lane;
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (c + j < w.n) y[(size_t)j * d] = v[i][j];
+            if (c + j < w.n) {
+              y[(size_t)j * d] = v0[i][j];
+              if (two) y[(size_t)j * d + 256] = v1[i][j];
+            }
         }
       }
       __syncwarp();
@@ -391,7 +387,6 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         atomicAdd(p.b.done + w.g, count);
         atomicAdd(p.b.done_all, count);
       }
-      __syncwarp();
     }
   }
   // the pair leaves together: the leader's MMAs read the peer's shared memory, and the peer's
@@ -399,7 +394,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  if (warp == 8) {
+  if (warp == kMxPairEpiWarps) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
   }

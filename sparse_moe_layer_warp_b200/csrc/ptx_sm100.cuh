@@ -408,6 +408,13 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
                : "memory");
 }
 
+// The same without release semantics: for an arrival that orders no memory accesses of this thread
+// (the release would wait for every store in flight).
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
 // TMA tile load for a CTA pair: the data lands in this CTA's shared memory, the transaction
 // bytes are counted on `bar_cluster` (the leader's barrier, a shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map,

@@ -14,13 +14,16 @@
 // all N columns are needed by both CTAs, those of the weight rows by the CTA that holds them.
 // The combine is a launch of its own: at these sizes y is larger than L2 and wants every warp.
 #pragma once
+#include <limits.h>
+
 #include "mxfp4_layer.cuh"
 
 namespace moe {
 
 constexpr int kMxPairEpiWarps = 16;  // warps 0-15: four for each TMEM lane quadrant
-// then MMA, two warps for the weights, token rows, scheduler
-constexpr int kMxPairThreads = 32 * (kMxPairEpiWarps + 5);
+// then the leader's MMA, the peer's scheduler; two warps for the weights; token rows.  20 warps: a
+// 21st would leave 80 registers a thread, and the epilogue spilled.
+constexpr int kMxPairThreads = 32 * (kMxPairEpiWarps + 4);
 
 struct MxPairParams {
   StreamBase b;
@@ -81,7 +84,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   uint64_t *tfull = empty + S;
   uint64_t *tempty = tfull + 1;             // the leader's: both CTAs' epilogue warps
   uint64_t *uq_full = tempty + 1;
-  uint64_t *uq_empty = uq_full + kUnitQ;    // the leader's: both CTAs' readers
+  uint64_t *uq_empty = uq_full + kUnitQ;    // the peer's: both CTAs' readers
   uint64_t *mma_end = uq_empty + kUnitQ;
   Unit *uq = reinterpret_cast<Unit *>(mma_end + 1);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(uq + kUnitQ);
@@ -130,14 +133,17 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   };
   int qi = 0;
   uint32_t qph = 0;
-  const uint32_t uq_empty_leader = mapa_shared(smem_u32(uq_empty), 0);
+  const uint32_t uq_empty_peer = mapa_shared(smem_u32(uq_empty), 1);
   auto next_unit = [&](Unit &w, int where) -> bool {
     if (!__all_sync(0xffffffffu, mbar_wait_suspend<true>(&uq_full[qi], qph, abort_flag,
                                                          p.b.status, where)))
       return false;
     w = uq[qi];
-    __syncwarp();
-    if (lane == 0) mbar_arrive_remote(uq_empty_leader + qi * 8);
+    // The arrival has no release (it would wait for the epilogue's stores in flight, 2500 clocks a
+    // unit); its address depends on every word read, so it cannot pass the reads.
+    const int all = w.kind | w.g | w.mt | w.tok0 | w.n | w.row0 | w.uses | w.rows | w.tile;
+    const bool read = __all_sync(0xffffffffu, all != INT_MIN);
+    if (lane == 0) mbar_arrive_remote_relaxed(uq_empty_peer + (read ? qi : 0) * 8);
     if (++qi == kUnitQ) {
       qi = 0;
       qph ^= 1;
@@ -150,21 +156,22 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   };
   bool alive = true;
 
-  if (warp == kMxPairEpiWarps + 4) {
-    if (lane == 0 && leader)
+  if (warp == kMxPairEpiWarps && !leader) {
+    // ---------------------------------------------------------------- scheduler (peer)
+    if (lane == 0)
       schedule_units(p.b, tb, BN, up_tiles, down_tiles, blockIdx.x >> 1, gridDim.x >> 1,
                      [&](const Unit &r) {
                        if (!mbar_wait_suspend<true>(&uq_empty[qi], qph ^ 1, abort_flag, p.b.status,
                                                     31))
                          return false;
                        uq[qi] = r;
-                       const uint32_t to = mapa_shared(smem_u32(&uq[qi]), 1);
+                       const uint32_t to = mapa_shared(smem_u32(&uq[qi]), 0);
                        const int *v = reinterpret_cast<const int *>(&r);
 #pragma unroll
                        for (int i = 0; i < (int)(sizeof(Unit) / 4); ++i)
                          st_shared_remote(to + 4 * i, v[i]);
                        mbar_arrive(&uq_full[qi]);
-                       mbar_arrive_remote(mapa_shared(smem_u32(&uq_full[qi]), 1));
+                       mbar_arrive_remote(mapa_shared(smem_u32(&uq_full[qi]), 0));
                        if (++qi == kUnitQ) {
                          qi = 0;
                          qph ^= 1;
@@ -260,61 +267,59 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     __syncwarp();
   } else if (warp == kMxPairEpiWarps) {
     // ---------------------------------------------------------------- MMA (leader)
-    if (leader) {
-      int st = 0, it = 0;
-      uint32_t ph = 0;
-      Unit w;
-      const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem_base);
-      const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB), sa_base = smem_u32(sSA),
-                     sb_base = smem_u32(sSB);
-      while (next_unit(w, 36)) {
-        const int kind = __reduce_max_sync(0xffffffffu, w.kind);
-        if (kind < 0) break;
-        const int nk = (kind == 0 ? d : f) / 128;
-        const int half = scale_lo_row(__reduce_max_sync(0xffffffffu, w.n), BN);
-        const bool two = kind == 0 || __reduce_max_sync(0xffffffffu, w.mt) * 512 + 256 < d;
-        bool ok = warp_wait(tempty, (it & 1) ^ 1, 46);
-        ++it;
-        tc_fence_after();
-        for (int kc = 0; ok && kc < nk; ++kc) {
-          ok = warp_wait(&full[st], ph, 37);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t sf = tm + C::ACC_COLS + (kc & 1) * C::SF_COLS;
-          const uint32_t sa = sa_base + st * C::SA_BYTES, sb = sb_base + st * C::SB_BYTES;
-          if (elect_one()) {
-            tc_cp_scales_pair(sf, sa);
-            if (two) tc_cp_scales_pair(sf + 4, sa + kMxScaleBlock);
-            tc_cp_scales_pair(sf + 8, sb);
-            if (half > 64) tc_cp_scales_pair(sf + 12, sb + kMxScaleBlock);
-            const uint64_t a = sdesc_k_sw128(a_base + st * C::A_BYTES),
-                           a2 = sdesc_k_sw128(a_base + st * C::A_BYTES + C::A_BYTES / 2),
-                           b = sdesc_k_sw128(b_base + st * C::B_BYTES);
-            const uint32_t id0 = idesc_mx(256, 2 * half);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t id = id0 | ((uint32_t)kk << 4) | ((uint32_t)kk << 29);
-              const uint32_t add = (kc | kk) ? 1u : 0u;
-              tc_mma_mx_pair(tm, a + 2 * kk, b + 2 * kk, id, sf, sf + 8, add);
-              if (two) tc_mma_mx_pair(tm + C::TILE_COLS, a2 + 2 * kk, b + 2 * kk, id, sf + 4,
-                                      sf + 8, add);
-            }
-            tc_commit_pair_both(&empty[st]);
-            if (kc == nk - 1) tc_commit_pair_both(tfull);
-          }
-          __syncwarp();
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
-          }
-        }
+    int st = 0, it = 0;
+    uint32_t ph = 0;
+    Unit w;
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem_base);
+    const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB), sa_base = smem_u32(sSA),
+                   sb_base = smem_u32(sSB);
+    while (next_unit(w, 36)) {
+      const int kind = __reduce_max_sync(0xffffffffu, w.kind);
+      if (kind < 0) break;
+      const int nk = (kind == 0 ? d : f) / 128;
+      const int half = scale_lo_row(__reduce_max_sync(0xffffffffu, w.n), BN);
+      const bool two = kind == 0 || __reduce_max_sync(0xffffffffu, w.mt) * 512 + 256 < d;
+      bool ok = warp_wait(tempty, (it & 1) ^ 1, 46);
+      ++it;
+      tc_fence_after();
+      for (int kc = 0; ok && kc < nk; ++kc) {
+        ok = warp_wait(&full[st], ph, 37);
         if (!ok) break;
+        tc_fence_after();
+        const uint32_t sf = tm + C::ACC_COLS + (kc & 1) * C::SF_COLS;
+        const uint32_t sa = sa_base + st * C::SA_BYTES, sb = sb_base + st * C::SB_BYTES;
+        if (elect_one()) {
+          tc_cp_scales_pair(sf, sa);
+          if (two) tc_cp_scales_pair(sf + 4, sa + kMxScaleBlock);
+          tc_cp_scales_pair(sf + 8, sb);
+          if (half > 64) tc_cp_scales_pair(sf + 12, sb + kMxScaleBlock);
+          const uint64_t a = sdesc_k_sw128(a_base + st * C::A_BYTES),
+                         a2 = sdesc_k_sw128(a_base + st * C::A_BYTES + C::A_BYTES / 2),
+                         b = sdesc_k_sw128(b_base + st * C::B_BYTES);
+          const uint32_t id0 = idesc_mx(256, 2 * half);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint32_t id = id0 | ((uint32_t)kk << 4) | ((uint32_t)kk << 29);
+            const uint32_t add = (kc | kk) ? 1u : 0u;
+            tc_mma_mx_pair(tm, a + 2 * kk, b + 2 * kk, id, sf, sf + 8, add);
+            if (two) tc_mma_mx_pair(tm + C::TILE_COLS, a2 + 2 * kk, b + 2 * kk, id, sf + 4,
+                                    sf + 8, add);
+          }
+          tc_commit_pair_both(&empty[st]);
+          if (kc == nk - 1) tc_commit_pair_both(tfull);
+        }
+        __syncwarp();
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
+        }
       }
-      if (lane == 0) {
-        tc_commit_pair_local(mma_end);
-        volatile int no_abort = 0;
-        mbar_wait_bounded(mma_end, 0, &no_abort, nullptr, 0);
-      }
+      if (!ok) break;
+    }
+    if (lane == 0) {
+      tc_commit_pair_local(mma_end);
+      volatile int no_abort = 0;
+      mbar_wait_bounded(mma_end, 0, &no_abort, nullptr, 0);
     }
     __syncwarp();
   } else if (warp < kMxPairEpiWarps) {

@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     mxfp4_layer_kernel(const __grid_constant__ MxParams p) {
   using C = MxCfg<BN>;
   constexpr int S = C::STAGES, N = C::N;
+  constexpr int kRowArrivals = kRoute ? 32 : 1;  // of the token rows' warp at a stage
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 3);  // weights (two warps), token rows
+      mbar_init(&full[s], 2 + kRowArrivals);  // weights (two warps), token rows
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   uint32_t qph = 0;
   auto next_unit = [&](Unit &w, int where) -> bool {
     if (!warp_wait(&uq_full[qi], qph, where)) return false;
-    w = uq[qi];
+    w = load_unit(&uq[qi]);
     __syncwarp();
     if (lane == 0) mbar_arrive(&uq_empty[qi]);
     if (++qi == kUnitQ) {
@@ -418,28 +419,27 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     __syncwarp();
   } else if (warp == 5 || warp == 6) {
     // ---------------------------------------------------------------- weights
-    // One warp for each of a stage's two tiles: issuing a copy takes a thread about 70 ns, waiting
-    // for the slot and announcing the bytes 150 ns more.
-    const int half = warp - 5;
+    // One warp for each of a stage's two tiles.
+    const int half = __reduce_max_sync(0xffffffffu, warp) - 5;
     const uint64_t pol_once = policy_evict_first(), pol_reuse = policy_evict_last();
     int st = 0, filled = 0;
     uint32_t ph = 0;
     Unit w;
     bool ok = true;
     while ((ok = next_unit(w, 45)) && w.kind >= 0) {
-      if (lane == 0) {
-        const bool up = w.kind == 0;
-        const int nk = (up ? d : f) / 128, m_rows = up ? f : d;
-        const int tile = up ? w.mt : 2 * w.mt + half;
-        const bool there = tile * kMxTile < m_rows;  // d may be an odd number of tiles
-        const int row = w.g * m_rows + tile * kMxTile;
-        const CUtensorMap *m = up ? (half ? &p.tm_u : &p.tm_g) : &p.tm_d;
-        const uint8_t *sc = (up ? (half ? p.sc_u : p.sc_g) : p.sc_d) +
-                            (size_t)(row / kMxTile) * nk * kMxScaleBlock;
-        const uint64_t pol = w.uses == 1 ? pol_once : pol_reuse;
-        for (int kc = 0; kc < nk; ++kc) {
-          ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 32);
-          if (!ok) break;
+      const bool up = w.kind == 0;
+      const int nk = (up ? d : f) / 128, m_rows = up ? f : d;
+      const int tile = up ? w.mt : 2 * w.mt + half;
+      const bool there = tile * kMxTile < m_rows;  // d may be an odd number of tiles
+      const int row = w.g * m_rows + tile * kMxTile;
+      const CUtensorMap *m = up ? (half ? &p.tm_u : &p.tm_g) : &p.tm_d;
+      const uint8_t *sc = (up ? (half ? p.sc_u : p.sc_g) : p.sc_d) +
+                          (size_t)(row / kMxTile) * nk * kMxScaleBlock;
+      const uint64_t pol = w.uses == 1 ? pol_once : pol_reuse;
+      for (int kc = 0; kc < nk; ++kc) {
+        ok = warp_wait(&empty[st], ph ^ 1, 32);
+        if (!ok) break;
+        if (elect_one()) {
           if (there) {
             mbar_arrive_expect_tx(&full[st], kMxTile * 64 + kMxScaleBlock);
             tma_load_2d_hint(sA + st * C::A_BYTES + half * (C::A_BYTES / 2), m, &full[st],
@@ -449,14 +449,14 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           } else {
             mbar_arrive(&full[st]);
           }
-          ++filled;
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
-          }
+        }
+        __syncwarp();
+        ++filled;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
     }
     if (!ok && lane == 0) drain_stages(full, filled, S);
@@ -466,38 +466,19 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     // The rows of a unit are neighbours (x was split into sorted rows): a stage's come in one box,
     // its scales in one block.  Only x of the one-launch layer is by token: its rows are gathered
     // by 16-byte asynchronous copies, 8 lanes a row, into the swizzled tile, the scale words by
-    // 4-byte copies; the copies of up to kAhead stages are in flight, and one lane announces a
-    // stage when they have landed.  Nothing is held back while the warp waits: it announces
-    // everything first.
-    constexpr int kAhead = 3;
+    // 4-byte copies.  Every lane's copies arrive on the stage's barrier by themselves: a warp that
+    // waited for them to land before it announced a stage filled one slot in a copy's latency.
     const int h_target = n_rows * up_tiles * 4;
     bool all_ready = false;
-    int st = 0, pending = 0, filled = 0;
+    int st = 0, filled = 0;
     uint32_t ph = 0;
     Unit w;
     bool ok = true;
-    auto announce = [&](int n) {  // the n oldest pending stages, whose copies have landed
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMA reads them
-      __syncwarp();
-      if (lane == 0)
-        for (int i = 0; i < n; ++i) {
-          const int s = st - pending + i;
-          mbar_arrive(&full[s < 0 ? s + S : s]);
-        }
-      pending -= n;
-    };
-    auto flush = [&]() {
-      if (pending == 0) return;
-      cp_async_wait<0>();
-      announce(pending);
-    };
     while (true) {
-      if (!__all_sync(0xffffffffu, mbar_try_wait(&uq_full[qi], qph))) flush();
       ok = next_unit(w, 33);
       if (!ok || w.kind < 0) break;
       const bool up = w.kind == 0;
       if (!up && !all_ready) {
-        flush();
         // lane 0 waits for the group's h; lane 1 looks whether all of h is there, after which
         // no unit asks again (each look costs an L2 round trip)
         int got = 1;
@@ -513,27 +494,24 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       }
       const int K = up ? d : f, nk = K / 128;
       if (!kRoute || !up) {
-        flush();
-        if (lane == 0) {
-          const CUtensorMap *m = up ? &p.tm_x : &p.tm_h;
-          const uint8_t *sc = (up ? p.xs : p.hs) + (size_t)w.tile * nk * C::SB_BYTES;
-          for (int kc = 0; kc < nk; ++kc) {
-            ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 35);
-            if (!ok) break;
+        const CUtensorMap *m = up ? &p.tm_x : &p.tm_h;
+        const uint8_t *sc = (up ? p.xs : p.hs) + (size_t)w.tile * nk * C::SB_BYTES;
+        for (int kc = 0; kc < nk; ++kc) {
+          ok = warp_wait(&empty[st], ph ^ 1, 35);
+          if (!ok) break;
+          if (elect_one()) {
+            if (kRowArrivals > 1) mbar_arrive_n(&full[st], kRowArrivals - 1);
             mbar_arrive_expect_tx(&full[st], C::B_BYTES + C::SB_BYTES);
             tma_load_3d(sB + st * C::B_BYTES, m, &full[st], kc * 128, w.row0, 0);
             bulk_load(sSB + st * C::SB_BYTES, sc + kc * C::SB_BYTES, C::SB_BYTES, &full[st]);
-            ++filled;
-            if (++st == S) {
-              st = 0;
-              ph ^= 1;
-            }
+          }
+          __syncwarp();
+          ++filled;
+          if (++st == S) {
+            st = 0;
+            ph ^= 1;
           }
         }
-        st = __shfl_sync(0xffffffffu, st, 0);
-        ph = __shfl_sync(0xffffffffu, ph, 0);
-        filled = __shfl_sync(0xffffffffu, filled, 0);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) break;
         continue;
       }
@@ -541,11 +519,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       int my_row = w.row0 + lane;
       if (lane < w.n) my_row = w.g < p.b.E ? perm[w.row0 + lane] / p.b.k : w.tok0 + lane;
       for (int kc = 0; kc < nk; ++kc) {
-        if (!__all_sync(0xffffffffu, mbar_try_wait(&empty[st], ph ^ 1))) {
-          flush();
-          ok = warp_wait(&empty[st], ph ^ 1, 35);
-          if (!ok) break;
-        }
+        ok = warp_wait(&empty[st], ph ^ 1, 35);
+        if (!ok) break;
         const uint32_t b = smem_u32(sB) + st * C::B_BYTES, sb = smem_u32(sSB) + st * C::SB_BYTES;
         const int c = lane & 7;  // 16-byte chunk of a 128-byte row
         for (int r0 = 0; r0 < 2 * w.n; r0 += 4) {
@@ -563,28 +538,20 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             cp_async4(sb + scale_row_at(r < w.n ? r : BN + i),
                       p.xs + (row * nk + kc) * 8 + (r < w.n ? 0 : 4));
         }
-        cp_async_commit();
-        ++pending;
+        cp_async_arrive(&full[st]);
         ++filled;
         if (++st == S) {
           st = 0;
           ph ^= 1;
         }
-        if (pending == kAhead) {
-          cp_async_wait<kAhead - 1>();
-          announce(1);
-        }
       }
       if (!ok) break;
     }
-    flush();
+    cp_async_wait_all();
     if (!ok && lane == 0) drain_stages(full, filled, S);
     __syncwarp();
   } else if (warp == 4) {
     // ---------------------------------------------------------------- MMA
-    // The warp stays together and one elected lane issues: with the operands of the instructions in
-    // uniform registers an issue takes a few clocks.  (Under `if (lane == 0)` each of a stage's 11
-    // tcgen05 operations took 70, twice the time of the products at 16 tokens.)
     int st = 0, it = 0;
     uint32_t ph = 0;
     Unit w;
@@ -592,10 +559,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB), sa_base = smem_u32(sSA),
                    sb_base = smem_u32(sSB);
     while (next_unit(w, 36)) {
-      const int kind = __reduce_max_sync(0xffffffffu, w.kind);
+      const int kind = w.kind;
       if (kind < 0) break;
       const int acc = it & 1, nk = (kind == 0 ? d : f) / 128;
-      const bool two = kind == 0 || (2 * __reduce_max_sync(0xffffffffu, w.mt) + 1) * kMxTile < d;
+      const bool two = kind == 0 || (2 * w.mt + 1) * kMxTile < d;
       bool ok = warp_wait(&tempty[acc], ((it >> 1) & 1) ^ 1, 46);
       tc_fence_after();
       const uint32_t d0 = tm + acc * C::ACC_COLS;
@@ -606,6 +573,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         const uint32_t sf = tm + 2 * C::ACC_COLS + (kc & 1) * C::SF_COLS;
         const uint32_t sa = sa_base + st * C::SA_BYTES;
         if (elect_one()) {
+          // gathered token rows: written by the copies' generic proxy, read by the tensor cores
+          if (kRoute) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           tc_cp_scales(sf, sa);
           if (two) tc_cp_scales(sf + 4, sa + kMxScaleBlock);
           tc_cp_scales(sf + 8, sb_base + st * C::SB_BYTES);

@@ -133,16 +133,17 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   };
   int qi = 0;
   uint32_t qph = 0;
+  const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
   const uint32_t uq_empty_peer = mapa_shared(smem_u32(uq_empty), 1);
   auto next_unit = [&](Unit &w, int where) -> bool {
     if (!__all_sync(0xffffffffu, mbar_wait_suspend<true>(&uq_full[qi], qph, abort_flag,
                                                          p.b.status, where)))
       return false;
-    w = uq[qi];
+    w = load_unit(&uq[qi]);
     // The arrival has no release (it would wait for the epilogue's stores in flight, 2500 clocks a
     // unit); its address depends on every word read, so it cannot pass the reads.
     const int all = w.kind | w.g | w.mt | w.tok0 | w.n | w.row0 | w.uses | w.rows | w.tile;
-    const bool read = __all_sync(0xffffffffu, all != INT_MIN);
+    const bool read = all != INT_MIN;
     if (lane == 0) mbar_arrive_remote_relaxed(uq_empty_peer + (read ? qi : 0) * 8);
     if (++qi == kUnitQ) {
       qi = 0;
@@ -182,44 +183,44 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   } else if (warp == kMxPairEpiWarps + 1 || warp == kMxPairEpiWarps + 2) {
     // ---------------------------------------------------------------- weights
     // Warp j: tile j of the unit.
-    const int j = warp - (kMxPairEpiWarps + 1);
+    const int j = __reduce_max_sync(0xffffffffu, warp) - (kMxPairEpiWarps + 1);
     const uint64_t pol_once = policy_evict_first(), pol_reuse = policy_evict_last();
     int st = 0, filled = 0;
     uint32_t ph = 0;
     Unit w;
     bool ok = true;
     while ((ok = next_unit(w, 45)) && w.kind >= 0) {
-      if (lane == 0) {
-        const bool up = w.kind == 0;
-        const int nk = (up ? d : f) / 128, m_rows = up ? f : d;
-        const bool there = tile_row(w, j, rank) < m_rows;
-        const int row = w.g * m_rows + tile_row(w, j, rank);
-        const uint32_t bytes = ((tile_row(w, j, 0) < m_rows) + (tile_row(w, j, 1) < m_rows)) *
-                               (kMxTile * 64 + kMxScaleBlock);  // of both CTAs
-        uint8_t *a = sA + j * (C::A_BYTES / 2), *sa = sSA + j * kMxScaleBlock;
-        const CUtensorMap *m = up ? (j ? &p.tm_u : &p.tm_g) : &p.tm_d;
-        const CUtensorMap *sc = up ? (j ? &p.tm_su : &p.tm_sg) : &p.tm_sd;
-        const uint64_t pol = w.uses == 1 ? pol_once : pol_reuse;
-        for (int kc = 0; kc < nk; ++kc) {
-          ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 32);
-          if (!ok) break;
+      const bool up = w.kind == 0;
+      const int nk = (up ? d : f) / 128, m_rows = up ? f : d;
+      const bool there = tile_row(w, j, rank) < m_rows;
+      const int row = w.g * m_rows + tile_row(w, j, rank);
+      const uint32_t bytes = ((tile_row(w, j, 0) < m_rows) + (tile_row(w, j, 1) < m_rows)) *
+                             (kMxTile * 64 + kMxScaleBlock);  // of both CTAs
+      uint8_t *a = sA + j * (C::A_BYTES / 2), *sa = sSA + j * kMxScaleBlock;
+      const CUtensorMap *m = up ? (j ? &p.tm_u : &p.tm_g) : &p.tm_d;
+      const CUtensorMap *sc = up ? (j ? &p.tm_su : &p.tm_sg) : &p.tm_sd;
+      const uint64_t pol = w.uses == 1 ? pol_once : pol_reuse;
+      for (int kc = 0; kc < nk; ++kc) {
+        ok = warp_wait(&empty[st], ph ^ 1, 32);
+        if (!ok) break;
+        if (elect_one()) {
           if (leader) {
             if (bytes) mbar_arrive_expect_tx(&full[st], bytes);
             else mbar_arrive(&full[st]);
           }
           if (there) {
-            const uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
+            const uint32_t bar = full_leader + st * 8;
             tma_load_2d_pair(a + st * C::A_BYTES, m, bar, kc * 128, row, pol);
             tma_load_2d_pair(sa + st * C::SA_BYTES, sc, bar, 0, row / kMxTile * nk + kc, pol);
           }
-          ++filled;
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
-          }
+        }
+        __syncwarp();
+        ++filled;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
     }
     if (!ok && lane == 0 && leader) drain_stages(full, filled, S);
@@ -234,33 +235,39 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     Unit w;
     bool ok = true;
     while ((ok = next_unit(w, 33)) && w.kind >= 0) {
-      if (lane == 0) {
-        const bool up = w.kind == 0;
-        if (!up && !all_ready) {
-          ok = counter_wait_bounded(p.b.done + w.g, w.rows * up_tiles * 8, abort_flag, p.b.status,
-                                    34);
-          all_ready = counter_load(p.b.done_all) == h_target;
-          fence_proxy_async_global();  // other CTAs' stores, read by TMA
-        }
-        const int nk = (up ? d : f) / 128, box = w.n > 56 ? 1 : 0;
-        const CUtensorMap *m = up ? &p.tm_x[box] : &p.tm_h[box], *sc = up ? &p.tm_xs : &p.tm_hs;
-        for (int kc = 0; ok && kc < nk; ++kc) {
-          ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 35);
-          if (!ok) break;
-          const uint32_t bar = mapa_shared(smem_u32(&full[st]), 0);
+      const bool up = w.kind == 0;
+      if (!up && !all_ready) {
+        int got = 1;
+        if (lane == 0)
+          got = counter_wait_bounded(p.b.done + w.g, w.rows * up_tiles * 8, abort_flag, p.b.status,
+                                     34);
+        if (lane == 1) got = counter_load(p.b.done_all) == h_target ? 2 : 1;
+        ok = __shfl_sync(0xffffffffu, got, 0) != 0;
+        if (!ok) break;
+        all_ready = __shfl_sync(0xffffffffu, got, 1) == 2;
+        __syncwarp();  // the elected lane's copies follow those two loads
+        fence_proxy_async_global();  // other CTAs' stores, read by TMA
+      }
+      const int nk = (up ? d : f) / 128, box = w.n > 56 ? 1 : 0;
+      const CUtensorMap *m = up ? &p.tm_x[box] : &p.tm_h[box], *sc = up ? &p.tm_xs : &p.tm_hs;
+      for (int kc = 0; kc < nk; ++kc) {
+        ok = warp_wait(&empty[st], ph ^ 1, 35);
+        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t bar = full_leader + st * 8;
           if (leader)
             mbar_arrive_expect_tx(&full[st], 2 * ((box ? 112 : 56) * 128 + C::SB_BYTES));
           tma_load_2d_pair(sB + st * C::B_BYTES, m, bar, kc * 128, (int)rank * n_rows + w.row0,
                            pol);
           tma_load_2d_pair(sSB + st * C::SB_BYTES, sc, bar, 0, (w.tile * nk + kc) * 2, pol);
-          ++filled;
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
-          }
+        }
+        __syncwarp();
+        ++filled;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
     }
     if (!ok && lane == 0 && leader) drain_stages(full, filled, S);
@@ -274,11 +281,11 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB), sa_base = smem_u32(sSA),
                    sb_base = smem_u32(sSB);
     while (next_unit(w, 36)) {
-      const int kind = __reduce_max_sync(0xffffffffu, w.kind);
+      const int kind = w.kind;
       if (kind < 0) break;
       const int nk = (kind == 0 ? d : f) / 128;
-      const int half = scale_lo_row(__reduce_max_sync(0xffffffffu, w.n), BN);
-      const bool two = kind == 0 || __reduce_max_sync(0xffffffffu, w.mt) * 512 + 256 < d;
+      const int half = scale_lo_row(w.n, BN);
+      const bool two = kind == 0 || w.mt * 512 + 256 < d;
       bool ok = warp_wait(tempty, (it & 1) ^ 1, 46);
       ++it;
       tc_fence_after();

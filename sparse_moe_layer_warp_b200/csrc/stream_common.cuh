@@ -65,6 +65,21 @@ struct Unit {
   int tile;  // number of the token tile (token_tile_number)
 };
 
+// A unit as the queue holds it, in uniform registers: every lane reads the same words, and the
+// compiler knows it.  Producers and the MMA warp stay converged and let one elected lane issue: a
+// copy or a tcgen05 operation whose operands are uniform issues in about 25 clocks, under
+// `if (lane == 0)` in 70 to 130 -- two copies and a wait a stage then bound the whole kernel (760
+// clocks a stage whatever its work).
+__device__ __forceinline__ Unit load_unit(const Unit *q) {
+  Unit w;
+  const int *src = reinterpret_cast<const int *>(q);
+  int *dst = reinterpret_cast<int *>(&w);
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(Unit) / sizeof(int)); ++i)
+    dst[i] = __reduce_max_sync(0xffffffffu, src[i]);
+  return w;
+}
+
 // Token tile i (of bt rows) of group g, whose first sorted row is off, has number off / bt + g + i:
 // distinct for all tiles (a group of n rows moves the quotient by n / bt at least, rounded down,
 // and g by one), below rows / bt + groups.
@@ -135,8 +150,20 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {  // 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
+// This thread's arrival on `bar` once its cp.async so far have landed (one of the expected arrivals).
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {  // all but the last N groups have landed

@@ -25,8 +25,7 @@ namespace moe {
 
 constexpr int kStreamWarps = 8;     // consumer warps: each an eighth of a stage's K
 constexpr int kStreamEpiWarps = 4;  // sum the partials of a unit, store, publish
-// weights (one warp for each half of a stage's rows: issuing a load takes a thread about 70 ns,
-// waiting and announcing it 150 ns more), token rows, scheduler
+// weights (one warp for each half of a stage's rows), token rows, scheduler
 constexpr int kStreamProdWarps = 4;
 constexpr int kStreamAllWarps = kStreamWarps + kStreamProdWarps + kStreamEpiWarps;
 constexpr int kStreamThreads = 32 * kStreamAllWarps;
@@ -152,7 +151,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
   uint32_t qph = 0;
   auto next_unit = [&](Unit &w, int where) -> bool {
     if (!warp_wait(&uq_full[qi], qph, where)) return false;
-    w = uq[qi];
+    w = load_unit(&uq[qi]);
     __syncwarp();
     if (lane == 0) mbar_arrive(&uq_empty[qi]);
     if (++qi == kUnitQ) {
@@ -168,35 +167,35 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     // ---------------------------------------------------------------- weight producers
     // Warp 0 loads the first half of a stage's rows (gate, or the first rows of W_d), warp 1 the
     // other (up, or the next rows).
-    const int half = warp - kStreamWarps;
+    const int half = __reduce_max_sync(0xffffffffu, warp) - kStreamWarps;
     const uint64_t pol_once = policy_evict_first(), pol_reuse = policy_evict_last();
     int st = 0, filled = 0;
     uint32_t ph = 0;
     bool ok = true;
     Unit w;
     while ((ok = next_unit(w, 45)) && w.kind >= 0) {
-      if (lane == 0) {
-        const bool up = w.kind == 0;
-        const int nch = up ? nch_up : nch_down;
-        const int row = w.g * (up ? f : d) + w.mt * (up ? C::UP_ROWS : C::DOWN_ROWS) +
-                        (up ? 0 : half * C::UP_ROWS);
-        const uint64_t pol = w.uses == 1 ? pol_once : pol_reuse;
-        const CUtensorMap *m = up ? (half ? &p.tm_u : &p.tm_g) : &p.tm_d;
-        for (int kc = 0; kc < nch; ++kc) {
-          ok = mbar_wait_suspend(&empty[st], ph ^ 1, abort_flag, p.b.status, 32);
-          if (!ok) break;
+      const bool up = w.kind == 0;
+      const int nch = up ? nch_up : nch_down;
+      const int row = w.g * (up ? f : d) + w.mt * (up ? C::UP_ROWS : C::DOWN_ROWS) +
+                      (up ? 0 : half * C::UP_ROWS);
+      const uint64_t pol = w.uses == 1 ? pol_once : pol_reuse;
+      const CUtensorMap *m = up ? (half ? &p.tm_u : &p.tm_g) : &p.tm_d;
+      for (int kc = 0; kc < nch; ++kc) {
+        ok = warp_wait(&empty[st], ph ^ 1, 32);
+        if (!ok) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&full[st], C::A_BYTES / 2);
           // a half's four tiles of 64 columns in one load; those past K are zero
           tma_load_3d_hint(sA + st * C::A_BYTES + half * (C::A_BYTES / 2), m, &full[st], 0, row,
                            kc * 4, pol);
-          ++filled;
-          if (++st == S) {
-            st = 0;
-            ph ^= 1;
-          }
+        }
+        __syncwarp();
+        ++filled;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1;
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) break;
     }
     if (!ok && lane == 0) drain_stages(full, filled, S);

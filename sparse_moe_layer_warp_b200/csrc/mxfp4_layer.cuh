@@ -30,8 +30,9 @@
 
 namespace moe {
 
-constexpr int kMxWarps = 16;  // 0-3 epilogue, 4 MMA, 5-6 weights, 7 token rows, 8 scheduler; the
-                              // others route (one-launch layer) and combine
+// 0-3 epilogue, 4-5 MMA, 6-7 weights, 8 token rows, 9 scheduler; the others route (one-launch layer)
+// and combine
+constexpr int kMxWarps = 16;
 constexpr int kMxThreads = 32 * kMxWarps;
 constexpr int kMxTile = 128;  // weight rows of a tile: h columns of an up unit
 constexpr int kMxDown = 2 * kMxTile;  // y columns of a down unit
@@ -77,7 +78,7 @@ struct MxCfg {
   static constexpr int SA_BYTES = 2 * kMxScaleBlock, SB_BYTES = scale_block_bytes(BN);
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
   static constexpr int ACC_COLS = 2 * N;           // both weight tiles
-  static constexpr int SF_COLS = 16;               // scale columns of a stage; two sets in turn
+  static constexpr int SF_COLS = 16;  // scale columns of a stage, 8 a weight tile; two sets in turn
   static constexpr int TMEM_USED = 2 * ACC_COLS + 2 * SF_COLS;
   static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : (TMEM_USED <= 256 ? 256 : 512);
   static_assert(TMEM_USED <= 512 && N % 16 == 0 && N <= 128 && B_BYTES % 1024 == 0, "tile");
@@ -324,17 +325,17 @@ __global__ void __launch_bounds__(kMxThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&full[s], 2 + kRowArrivals);  // weights (two warps), token rows
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);  // MMA warps
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&tfull[i], 1);
+      mbar_init(&tfull[i], 2);
       mbar_init(&tempty[i], 4);
     }
     for (int q = 0; q < kUnitQ; ++q) {
       mbar_init(&uq_full[q], 1);
-      mbar_init(&uq_empty[q], 8);  // epilogue 4, MMA, weights 2, token rows
+      mbar_init(&uq_empty[q], 9);  // epilogue 4, MMA 2, weights 2, token rows
     }
-    mbar_init(mma_end, 1);
+    mbar_init(mma_end, 2);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_g);
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
 
   if (!alive) {
     // the grid barrier gave up: no unit is claimed
-  } else if (warp == 8) {
+  } else if (warp == 9) {
     if (lane == 0)
       schedule_units(p.b, tb, BN, up_tiles, down_tiles, blockIdx.x, gridDim.x,
                      [&](const Unit &r) {
@@ -417,10 +418,10 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                        return true;
                      });
     __syncwarp();
-  } else if (warp == 5 || warp == 6) {
+  } else if (warp == 6 || warp == 7) {
     // ---------------------------------------------------------------- weights
     // One warp for each of a stage's two tiles.
-    const int half = __reduce_max_sync(0xffffffffu, warp) - 5;
+    const int half = __reduce_max_sync(0xffffffffu, warp) - 6;
     const uint64_t pol_once = policy_evict_first(), pol_reuse = policy_evict_last();
     int st = 0, filled = 0;
     uint32_t ph = 0;
@@ -461,7 +462,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     }
     if (!ok && lane == 0) drain_stages(full, filled, S);
     __syncwarp();
-  } else if (warp == 7) {
+  } else if (warp == 8) {
     // ---------------------------------------------------------------- token rows
     // The rows of a unit are neighbours (x was split into sorted rows): a stage's come in one box,
     // its scales in one block.  Only x of the one-launch layer is by token: its rows are gathered
@@ -515,28 +516,44 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         if (!ok) break;
         continue;
       }
-      // row of token i of the unit
+      // This lane's piece of the first 4 rows (hi, then lo) and its scale word: addresses once a
+      // unit, so that a unit of one or two tokens -- most are -- takes two copies a stage.
       int my_row = w.row0 + lane;
       if (lane < w.n) my_row = w.g < p.b.E ? perm[w.row0 + lane] / p.b.k : w.tok0 + lane;
+      const int c = lane & 7;  // 16-byte chunk of a 128-byte row
+      auto piece = [&](int r, uint32_t &to, const uint8_t *&src) {
+        const int i = r < w.n ? r : r - w.n, t = r < w.n ? r : BN + i;  // row of the tile
+        const size_t row = __shfl_sync(0xffffffffu, my_row, i & 31);
+        to = t * 128 + ((c ^ (t & 7)) << 4);
+        src = (r < w.n ? p.x.hi : p.x.lo) + row * K + c * 16;
+      };
+      auto word = [&](int r, uint32_t &to, const uint8_t *&src) {
+        const int i = r < w.n ? r : r - w.n;
+        const size_t row = __shfl_sync(0xffffffffu, my_row, i & 31);
+        to = scale_row_at(r < w.n ? r : BN + i);
+        src = p.xs + row * nk * 8 + (r < w.n ? 0 : 4);
+      };
+      uint32_t to0, to1;
+      const uint8_t *src0, *src1;
+      piece(lane >> 3, to0, src0);
+      word(lane, to1, src1);
       for (int kc = 0; kc < nk; ++kc) {
         ok = warp_wait(&empty[st], ph ^ 1, 35);
         if (!ok) break;
         const uint32_t b = smem_u32(sB) + st * C::B_BYTES, sb = smem_u32(sSB) + st * C::SB_BYTES;
-        const int c = lane & 7;  // 16-byte chunk of a 128-byte row
-        for (int r0 = 0; r0 < 2 * w.n; r0 += 4) {
-          const int r = r0 + (lane >> 3), i = r < w.n ? r : r - w.n;
-          const size_t row = __shfl_sync(0xffffffffu, my_row, i & 31);
-          const int to = r < w.n ? r : BN + i;  // row of the tile
-          if (r < 2 * w.n)
-            cp_async16(b + to * 128 + ((c ^ (to & 7)) << 4),
-                       (r < w.n ? p.x.hi : p.x.lo) + row * K + kc * 128 + c * 16);
+        if ((lane >> 3) < 2 * w.n) cp_async16(b + to0, src0 + kc * 128);
+        if (lane < 2 * w.n) cp_async4(sb + to1, src1 + kc * 8);
+        for (int r = 4 + (lane >> 3); r - (lane >> 3) < 2 * w.n; r += 4) {
+          uint32_t to;
+          const uint8_t *src;
+          piece(r, to, src);
+          if (r < 2 * w.n) cp_async16(b + to, src + kc * 128);
         }
-        for (int r0 = 0; r0 < 2 * w.n; r0 += 32) {
-          const int r = r0 + lane, i = r < w.n ? r : r - w.n;
-          const size_t row = __shfl_sync(0xffffffffu, my_row, i & 31);
-          if (r < 2 * w.n)
-            cp_async4(sb + scale_row_at(r < w.n ? r : BN + i),
-                      p.xs + (row * nk + kc) * 8 + (r < w.n ? 0 : 4));
+        for (int r = 32 + lane; r - lane < 2 * w.n; r += 32) {
+          uint32_t to;
+          const uint8_t *src;
+          word(r, to, src);
+          if (r < 2 * w.n) cp_async4(sb + to, src + kc * 8);
         }
         cp_async_arrive(&full[st]);
         ++filled;
@@ -550,52 +567,52 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     cp_async_wait_all();
     if (!ok && lane == 0) drain_stages(full, filled, S);
     __syncwarp();
-  } else if (warp == 4) {
+  } else if (warp == 4 || warp == 5) {
     // ---------------------------------------------------------------- MMA
+    // One warp for each weight tile: a stage's loop turn (the wait, 11 tcgen05 operations, the
+    // commit) takes one issuing thread 750 clocks, the products 330 at 16 columns.  The next stage's
+    // barrier is looked at before this one's products are issued.
+    const int j = __reduce_max_sync(0xffffffffu, warp) - 4;
     int st = 0, it = 0;
     uint32_t ph = 0;
     Unit w;
     const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem_base);
-    const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB), sa_base = smem_u32(sSA),
-                   sb_base = smem_u32(sSB);
-    while (next_unit(w, 36)) {
-      const int kind = w.kind;
-      if (kind < 0) break;
-      const int acc = it & 1, nk = (kind == 0 ? d : f) / 128;
-      const bool two = kind == 0 || (2 * w.mt + 1) * kMxTile < d;
+    const uint32_t a_base = smem_u32(sA) + j * (C::A_BYTES / 2), b_base = smem_u32(sB),
+                   sa_base = smem_u32(sSA) + j * kMxScaleBlock, sb_base = smem_u32(sSB);
+    while (next_unit(w, 36) && w.kind >= 0) {
+      const int acc = it & 1, nk = (w.kind == 0 ? d : f) / 128;
+      const bool there = j == 0 || w.kind == 0 || (2 * w.mt + 1) * kMxTile < d;
       bool ok = warp_wait(&tempty[acc], ((it >> 1) & 1) ^ 1, 46);
-      tc_fence_after();
-      const uint32_t d0 = tm + acc * C::ACC_COLS;
+      const uint32_t d0 = tm + acc * C::ACC_COLS + j * N;
+      bool ready = false;
       for (int kc = 0; ok && kc < nk; ++kc) {
-        ok = warp_wait(&full[st], ph, 37);
+        if (!__all_sync(0xffffffffu, ready)) ok = warp_wait(&full[st], ph, 37);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sf = tm + 2 * C::ACC_COLS + (kc & 1) * C::SF_COLS;
-        const uint32_t sa = sa_base + st * C::SA_BYTES;
+        const int st1 = st + 1 == S ? 0 : st + 1;
+        const uint32_t ph1 = st + 1 == S ? ph ^ 1 : ph;
+        ready = kc + 1 < nk && mbar_test_wait(&full[st1], ph1);
+        const uint32_t sf = tm + 2 * C::ACC_COLS + (kc & 1) * C::SF_COLS + j * 8;
         if (elect_one()) {
-          // gathered token rows: written by the copies' generic proxy, read by the tensor cores
-          if (kRoute) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          tc_cp_scales(sf, sa);
-          if (two) tc_cp_scales(sf + 4, sa + kMxScaleBlock);
-          tc_cp_scales(sf + 8, sb_base + st * C::SB_BYTES);
-          const uint64_t a = sdesc_k_sw128(a_base + st * C::A_BYTES),
-                         a2 = sdesc_k_sw128(a_base + st * C::A_BYTES + C::A_BYTES / 2),
-                         b = sdesc_k_sw128(b_base + st * C::B_BYTES);
+          if (there) {
+            // gathered token rows: written by the copies' generic proxy, read by the tensor cores
+            if (kRoute) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            tc_cp_scales(sf, sa_base + st * C::SA_BYTES);
+            tc_cp_scales(sf + 4, sb_base + st * C::SB_BYTES);
+            const uint64_t a = sdesc_k_sw128(a_base + st * C::A_BYTES),
+                           b = sdesc_k_sw128(b_base + st * C::B_BYTES);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of a row: 2 units of the descriptors
-            const uint32_t id = idesc_mx(kMxTile, N) | ((uint32_t)kk << 4) | ((uint32_t)kk << 29);
-            const uint32_t add = (kc | kk) ? 1u : 0u;
-            tc_mma_mx(d0, a + 2 * kk, b + 2 * kk, id, sf, sf + 8, add);
-            if (two) tc_mma_mx(d0 + N, a2 + 2 * kk, b + 2 * kk, id, sf + 4, sf + 8, add);
+            for (int kk = 0; kk < 4; ++kk)  // 32 bytes of a row: 2 units of the descriptors
+              tc_mma_mx(d0, a + 2 * kk, b + 2 * kk,
+                        idesc_mx(kMxTile, N) | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), sf,
+                        sf + 4, (kc | kk) ? 1u : 0u);
           }
           tc_commit(&empty[st]);
           if (kc == nk - 1) tc_commit(&tfull[acc]);
         }
         __syncwarp();
-        if (++st == S) {
-          st = 0;
-          ph ^= 1;
-        }
+        st = st1;
+        ph = ph1;
       }
       ++it;
       if (!ok) break;
@@ -674,8 +691,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     // ---------------------------------------------------------------- idle until the combine
     alive = warp_wait(mma_end, 0, 47);
   }
-  if (alive && (warp < 4 || warp > 8))
-    combine_pieces(p.b, slot_row, kMxDown, n_rows * 4, warp < 4 ? warp : warp - 5, kMxWarps - 5,
+  if (alive && (warp < 4 || warp > 9))
+    combine_pieces(p.b, slot_row, kMxDown, n_rows * 4, warp < 4 ? warp : warp - 6, kMxWarps - 6,
                    abort_flag);
   tc_fence_before();
   __syncthreads();

@@ -142,13 +142,16 @@ typedef struct {
 
 /* moe_layer_init over MXFP4 expert weights (cfg->dtype must be MOE_BF16, the type of the router
  * and the activations).  On such a handle moe_forward and moe_forward_few compute the layer above
- * with the weights' values as they stand (no rounding of x to fewer bits); the routing calls,
+ * with the weights' values as they stand; x is held as the sum of two e4m3 values under one
+ * power-of-two scale for 32 neighbours -- a bf16 value exactly, unless it is below 2^-13 of the
+ * largest of its block (then within 2^-21 of that largest) -- and h the same way, to 2^-9 of itself.
+ * An infinity in x or h counts as NaN, as it would after the down projection.  The routing calls,
  * moe_router_stats, moe_update_router_bias, the workspace and status calls and moe_set_option work as
  * on any handle (the launch-plan options change nothing).  Training, per-stage events and
  * expert health read bf16 weights: moe_backward*, moe_forward_save, moe_forward_profiled and
  * moe_expert_health return MOE_ERR_UNSUPPORTED, and so does moe_forward_partial.  Products are
- * accumulated in fp32; weights whose scale byte is 0 (2^-127) count as they stand only down to
- * fp32's smallest normal number. */
+ * accumulated in fp32.  Also MOE_ERR_UNSUPPORTED: max_tokens * (top_k + 1) * (d_ff / 32 + 8) of 2^31
+ * or more (4.9 million tokens at top-8 and d_ff 1280). */
 moe_status moe_layer_init_mxfp4(const moe_config *cfg, const moe_mxfp4_weights *w,
                                 moe_handle *out);
 
@@ -229,7 +232,7 @@ moe_status moe_forward(moe_handle h, const void *x, int n_tokens, void *out, voi
  * experts and combine in a persistent kernel that streams the chosen experts' weights without a
  * pause between the projections.  The same mathematics as moe_forward, and its selection bit for
  * bit; sums run in another fixed order (deterministic).  bf16 weights: h is rounded to bf16 as in
- * moe_forward; MXFP4: to 11 bits.  moe_forward of an MXFP4 handle is this call where it is
+ * moe_forward; MXFP4: as above.  moe_forward of an MXFP4 handle is this call where it is
  * supported.
  * At most 64 tokens, n_tokens * top_k <= 512, n_experts <= 288, d_model <= 8192; otherwise, and
  * for fp32 layers and expert-parallel slices, MOE_ERR_UNSUPPORTED.  A cooperative launch with one

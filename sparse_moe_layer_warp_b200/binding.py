@@ -6,7 +6,6 @@ the shared library is missing or fails to load, importing the functions raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -172,13 +171,20 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-_SAME_DEVICE = contextlib.nullcontext()
-
-
-def _on_device_of(t):
-    """Context in which t's device is current (entering one costs more than a small launch)."""
+def _call_on_device_of(t, fn, *args, stream=None) -> None:
+    """Library call `fn` with a last argument of the stream, with t's device current.  The device is
+    switched and the stream looked up only where needed: for a small matrix these take longer than
+    the kernel."""
     dev = t.get_device()
-    return _SAME_DEVICE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    call = getattr(load_library(), fn)
+    if dev == torch.cuda.current_device():
+        raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+        status = call(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            raw = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+            status = call(*args, raw)
+    _check(fn, status)
 
 
 # ------------------------------------------------------------------ C-ABI mirrors
@@ -448,12 +454,12 @@ def mxfp4_quantize(w, stream=None):
         raise ValueError(f"w: the last dimension must be a multiple of {MXFP4_BLOCK}, got shape "
                          f"{tuple(w.shape)}")
     _addr(w)
-    lead, cols = tuple(w.shape[:-1]), int(w.shape[-1])
-    codes = w.new_empty(lead + (cols // 2,), dtype=torch.uint8)
-    scales = w.new_empty(lead + (cols // MXFP4_BLOCK,), dtype=torch.uint8)
-    if w.numel():
-        with _on_device_of(w):
-            moe_mxfp4_quantize(w, codes, scales, stream)
+    lead, cols = w.shape[:-1], w.shape[-1]
+    codes = w.new_empty((*lead, cols // 2), dtype=torch.uint8)
+    scales = w.new_empty((*lead, cols // MXFP4_BLOCK), dtype=torch.uint8)
+    if n := w.numel():
+        _call_on_device_of(w, "moe_mxfp4_quantize", w.data_ptr(), _DTYPE_CODE[w.dtype], n // cols,
+                           cols, codes.data_ptr(), scales.data_ptr(), stream=stream)
     return codes, scales
 
 
@@ -471,9 +477,9 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
     if scales.device != codes.device:
         raise ValueError(f"scales: on {scales.device}, codes on {codes.device}")
     out = codes.new_empty(lead + (cols,), dtype=dtype)
-    if out.numel():
-        with _on_device_of(codes):
-            moe_mxfp4_dequantize(codes, scales, out, stream)
+    if n := out.numel():
+        _call_on_device_of(codes, "moe_mxfp4_dequantize", codes.data_ptr(), scales.data_ptr(),
+                           n // cols, cols, out.data_ptr(), _DTYPE_CODE[dtype], stream=stream)
     return out
 
 
@@ -509,6 +515,7 @@ class MoELayer:
         self.device = w_router.device
         self.dtype = w_router.dtype
         self.ws = None
+        self.ws_need = {}  # bytes by number of tokens
         self.bw_ws = None
         self.E, self.k, self.d = int(E), int(top_k), int(d)
 
@@ -533,7 +540,9 @@ class MoELayer:
         moe_set_option(self.handle, option, value)
 
     def workspace(self, n_tokens: int):
-        need = moe_workspace_size(self.handle, n_tokens)
+        need = self.ws_need.get(n_tokens)
+        if need is None:
+            need = self.ws_need[n_tokens] = moe_workspace_size(self.handle, n_tokens)
         if self.ws is None or self.ws.numel() < need:
             self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             moe_workspace_init(self.handle, self.ws)
@@ -733,6 +742,7 @@ class MoELayerMXFP4(MoELayer):
         self.device = w_router.device
         self.dtype = w_router.dtype
         self.ws = None
+        self.ws_need = {}  # bytes by number of tokens
         self.bw_ws = None
         self.E, self.k, self.d = int(E), int(top_k), int(d)
 

@@ -257,16 +257,20 @@ __global__ void __launch_bounds__(256)
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, nk = d / 128, n_warps = gridDim.x * 8;
   for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += n_warps) {
-    // lane j: row of slot j (the shared row last), its tile's number, its hi and lo rows in a block
-    int row = 0, tile = 0, r = 0, r_lo = 0;
-    if (lane < k + n_shared) {
-      const int g = lane < k ? idx[(size_t)t * k + lane] : E;
-      const int off = lane < k ? offsets[g] : T * k, rows = lane < k ? offsets[g + 1] - off : T;
-      row = lane < k ? slot_row[(size_t)t * k + lane] : T * k + t;
+    // lane j: row of slot j, its tile's number, its hi and lo rows in a block; the shared row (all 32
+    // lanes may have slots) beside them
+    auto place = [&](int g, int off, int rows, int row, int &tile, int &r, int &r_lo) {
       tile = token_tile_number(off, g, (row - off) / BN, BN);
       r = (row - off) % BN;
       r_lo = scale_lo_row(min(BN, rows - (row - off - r)), BN) + r;
+    };
+    int row = 0, tile = 0, r = 0, r_lo = 0, s_tile, s_r, s_lo;
+    if (lane < k) {
+      const int g = idx[(size_t)t * k + lane], off = offsets[g];
+      row = slot_row[(size_t)t * k + lane];
+      place(g, off, offsets[g + 1] - off, row, tile, r, r_lo);
     }
+    place(E, T * k, T, T * k + t, s_tile, s_r, s_lo);
     for (int c0 = 0; c0 < d; c0 += 512) {
       const int c = c0 + lane * 16;
       float v[16];
@@ -274,19 +278,21 @@ __global__ void __launch_bounds__(256)
       for (int i = 0; i < 16; ++i) v[i] = 0.f;
       if (c < d) load16(x + (size_t)t * d + c, v);
       uint4 hi, lo;
-      uint32_t s_hi, s_lo;
-      split_lane(v, hi, lo, s_hi, s_lo);
+      uint32_t w_hi, w_lo;  // scale words
+      split_lane(v, hi, lo, w_hi, w_lo);
       for (int j = 0; j < k + n_shared; ++j) {
-        const size_t rw = __shfl_sync(0xffffffffu, row, j);
-        const size_t tl = __shfl_sync(0xffffffffu, tile, j);
-        const int rj = __shfl_sync(0xffffffffu, r, j), lj = __shfl_sync(0xffffffffu, r_lo, j);
+        const bool slot = j < k;
+        const size_t rw = slot ? __shfl_sync(0xffffffffu, row, j) : T * k + t;
+        const size_t tl = slot ? __shfl_sync(0xffffffffu, tile, j) : s_tile;
+        const int rj = slot ? __shfl_sync(0xffffffffu, r, j) : s_r;
+        const int lj = slot ? __shfl_sync(0xffffffffu, r_lo, j) : s_lo;
         if (c >= d) continue;
         *reinterpret_cast<uint4 *>(out.hi + rw * d + c) = hi;
         *reinterpret_cast<uint4 *>(out.lo + rw * d + c) = lo;
         if ((lane & 7) < 2)
           *reinterpret_cast<uint32_t *>(xs + (tl * nk + (c >> 7)) * scale_block_bytes(BN) +
                                         scale_row_at((lane & 1) ? lj : rj)) =
-              (lane & 1) ? s_lo : s_hi;
+              (lane & 1) ? w_lo : w_hi;
       }
     }
   }

@@ -268,8 +268,7 @@ bool few_shape(const moe_config &c, int T) {
 
 // Token rows of a tile of the MXFP4 layer.
 int mx_token_tile(const moe_config &c, int T) {
-  if (few_shape(c, T)) return T <= 8 ? 8 : (T <= 16 ? 16 : 32);
-  return (long long)T * c.top_k <= 16ll * c.n_experts ? 32 : kMxPairBN;
+  return !few_shape(c, T) ? kMxPairBN : T <= 8 ? 8 : T <= 16 ? 16 : 32;
 }
 
 // mx: an MXFP4 handle's layout (x and h as pairs of e4m3 values with their scales; x by token for
@@ -1470,11 +1469,11 @@ moe_status launch_shared_side(const moe_layer *h, const void *x, int T, void *ws
   return cudaEventRecord(h->ev_join, sd) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 // ------------------------------------------------------------------ weight streaming
-// A persistent kernel over every SM; one_launch: its CTAs meet at a barrier of the grid, so all must
-// be resident at once.
+// A one-launch layer over every SM: its CTAs meet at a barrier of the grid, so all must be resident
+// at once.
 template <typename Params>
-moe_status launch_stream(const moe_layer *L, void (*kern)(const Params), const Params &p,
-                         int threads, size_t smem, bool one_launch, cudaStream_t st) {
+moe_status launch_one(const moe_layer *L, void (*kern)(const Params), const Params &p, int threads,
+                      size_t smem, cudaStream_t st) {
   if (smem > (size_t)L->smem_optin) return MOE_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
@@ -1486,13 +1485,8 @@ moe_status launch_stream(const moe_layer *L, void (*kern)(const Params), const P
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
-  if (one_launch) {
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-  } else {
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-  }
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -1529,12 +1523,12 @@ StreamBase stream_base(const moe_layer *L, const void *x, int T, void *out, void
   return p;
 }
 
-// MXFP4 layer, token tiles of BN rows.
-template <int BN, bool kRoute>
-moe_status launch_mx(const moe_layer *L, const void *x, int T, void *out, void *ws,
+// MXFP4 layer in one launch, token tiles of BN rows.
+template <int BN>
+moe_status launch_mx_few(const moe_layer *L, const void *x, int T, void *out, void *ws,
                      const WsLayout &W, cudaStream_t st) {
   const moe_config &c = L->cfg;
-  const size_t P = (size_t)T * (c.top_k + c.n_shared), x_rows = kRoute ? (size_t)T : P;
+  const size_t P = (size_t)T * (c.top_k + c.n_shared);
   MxParams p;
   memset(&p, 0, sizeof p);
   p.b = stream_base(L, x, T, out, ws, W);
@@ -1544,15 +1538,12 @@ moe_status launch_mx(const moe_layer *L, const void *x, int T, void *out, void *
   p.sc_g = L->sc_gate;
   p.sc_u = L->sc_up;
   p.sc_d = L->sc_down;
-  p.x = split_rows(at<uint8_t>(ws, W.x_split), x_rows, c.d_model);
+  p.x = split_rows(at<uint8_t>(ws, W.x_split), T, c.d_model);
   p.h = split_rows(at<uint8_t>(ws, W.h), P, c.d_ff);
   p.xs = at<uint8_t>(ws, W.x_scale);
   p.hs = at<uint8_t>(ws, W.h_scale);
-  if ((!kRoute && !encode_split(&p.tm_x, p.x.hi, c.d_model, P, BN)) ||
-      !encode_split(&p.tm_h, p.h.hi, c.d_ff, P, BN))
-    return MOE_ERR_CUDA;
-  return launch_stream(L, mxfp4_layer_kernel<BN, kRoute>, p, kMxThreads, MxCfg<BN>::SMEM, kRoute,
-                       st);
+  if (!encode_split(&p.tm_h, p.h.hi, c.d_ff, P, BN)) return MOE_ERR_CUDA;
+  return launch_one(L, mxfp4_layer_kernel<BN>, p, kMxThreads, MxCfg<BN>::SMEM, st);
 }
 
 // 512-byte scale blocks [n] as words -> map with box {a block's 128 words, box_blocks}.
@@ -1608,8 +1599,7 @@ moe_status launch_bf16_few(const moe_layer *L, const void *x, int T, void *out, 
   p.tm_u = L->tm_st_u;
   p.tm_d = L->tm_st_d;
   p.h = at<__nv_bfloat16>(ws, W.h);
-  return launch_stream(L, weight_stream_kernel<NT>, p, kStreamThreads, StreamCfg<NT>::SMEM, true,
-                       st);
+  return launch_one(L, weight_stream_kernel<NT>, p, kStreamThreads, StreamCfg<NT>::SMEM, st);
 }
 
 // The whole layer in one launch (few_shape).
@@ -1620,10 +1610,10 @@ moe_status forward_few(const moe_layer *L, const void *x, int T, void *out, void
     return T <= 8 ? launch_bf16_few<1>(L, x, T, out, ws, W, st)
                   : launch_bf16_few<2>(L, x, T, out, ws, W, st);
   switch (mx_token_tile(L->cfg, T)) {
-    case 8: return launch_mx<8, true>(L, x, T, out, ws, W, st);
-    case 16: return launch_mx<16, true>(L, x, T, out, ws, W, st);
+    case 8: return launch_mx_few<8>(L, x, T, out, ws, W, st);
+    case 16: return launch_mx_few<16>(L, x, T, out, ws, W, st);
   }
-  return launch_mx<32, true>(L, x, T, out, ws, W, st);
+  return launch_mx_few<32>(L, x, T, out, ws, W, st);
 }
 
 // moe_forward of an MXFP4 handle.
@@ -1648,11 +1638,10 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
                   dim3(grid_for((size_t)T, 8, L->num_sms)), dim3(256), 0, st,
                   static_cast<const __nv_bfloat16 *>(x), at<int>(ws, W.slot_row),
                   at<int>(ws, W.idx), at<int>(ws, W.offsets), T, c.d_model, c.n_experts, c.top_k,
-                  c.n_shared, mx_token_tile(c, T),
+                  c.n_shared, kMxPairBN,
                   split_rows(at<uint8_t>(ws, W.x_split), P, c.d_model),
                   at<uint8_t>(ws, W.x_scale))) != MOE_OK)
     return s;
-  if (mx_token_tile(c, T) != kMxPairBN) return launch_mx<32, false>(L, x, T, out, ws, W, st);
   if ((s = launch_mx_pair(L, x, T, out, ws, W, st)) != MOE_OK) return s;
   return launch(mxfp4_combine_kernel,
                 dim3(grid_for((size_t)T * (c.d_model / 4), 256, L->num_sms)), dim3(256), 0, st,
@@ -1664,7 +1653,7 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
 int mxfp4_launches(const moe_layer *L, int T) {
   if (T == 0) return 0;
   if (few_shape(L->cfg, T)) return 1;
-  return (T <= kChunk ? 2 : 3) + (mx_token_tile(L->cfg, T) == kMxPairBN ? 3 : 2);
+  return (T <= kChunk ? 2 : 3) + 3;  // routing; split rows, experts, combine
 }
 }  // namespace
 

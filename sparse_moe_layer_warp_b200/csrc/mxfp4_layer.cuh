@@ -1,5 +1,6 @@
-// mxfp4_layer.cuh -- the experts (and, for a few tokens, the whole layer) over MXFP4 weights in one
-// persistent kernel on the block-scaled tensor cores.
+// mxfp4_layer.cuh -- the whole layer for a few tokens over MXFP4 weights in one persistent kernel on
+// the block-scaled tensor cores (stream_common.cuh: units, waits, routing), and what it shares with
+// the CTA-pair kernel for more tokens (mxfp4_pair.cuh).
 //
 // Arithmetic.  The weights' e2m1 codes and e8m0 scales go to tcgen05.mma (.kind::mxf8f6f4,
 // .block_scale) as they are: no unpacking by the CUDA cores.  The other operand of that
@@ -63,11 +64,11 @@ __device__ __forceinline__ int scale_row_at(int r) {
 struct MxParams {
   StreamBase b;
   CUtensorMap tm_g, tm_u, tm_d;              // codes, box {128, 128}, padded 4-bit
-  CUtensorMap tm_x, tm_h;                    // token rows: box {128, BN, hi and lo}
+  CUtensorMap tm_h;                          // rows of h: box {128, BN, hi and lo}
   const uint8_t *sc_g, *sc_u, *sc_d;         // scale blocks (mxfp4_tile_scales_kernel)
-  SplitRows x, h;                            // x: rows by token (one-launch layer), or sorted
-  uint8_t *xs, *hs;                          // scale blocks by token tile and 128 columns; one-
-                                             // launch layer: xs words by token and 128 columns
+  SplitRows x, h;                            // x: rows by token
+  uint8_t *xs;                               // scale words of x by token and 128 columns
+  uint8_t *hs;                               // scale blocks of h by token tile and 128 columns
 };
 
 template <int BN>
@@ -298,12 +299,12 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <int BN, bool kRoute>
+template <int BN>
 __global__ void __launch_bounds__(kMxThreads, 1)
     mxfp4_layer_kernel(const __grid_constant__ MxParams p) {
   using C = MxCfg<BN>;
   constexpr int S = C::STAGES, N = C::N;
-  constexpr int kRowArrivals = kRoute ? 32 : 1;  // of the token rows' warp at a stage
+  constexpr int kRowArrivals = 32;  // of the token rows' warp at a stage: one a lane
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -349,13 +350,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     tma_prefetch_desc(&p.tm_d);
   }
   if (warp == 4) tmem_alloc(tmem_slot, C::TMEM_COLS);
-  const int *perm = kRoute ? tb.perm : p.b.perm;
-  const int *slot_row = kRoute ? tb.slot : p.b.slot_row;
-  const float *gate = kRoute ? tb.gate : p.b.gate;
-  bool alive = true;
   __syncthreads();  // the abort flag is clear
-  if (kRoute) {
-    // split x by token, then route; the ring's memory is the scratch
+  // split x by token, then route; the ring's memory is the scratch
+  {
     const int nk = d / 128, chunks = (d + 511) / 512, n_warps = gridDim.x * kMxWarps;
     for (int i = blockIdx.x * kMxWarps + warp; i < p.b.T * chunks; i += n_warps) {
       const int t = i / chunks, c = (i % chunks) * 512 + lane * 16;
@@ -373,16 +370,12 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         *reinterpret_cast<uint2 *>(p.xs + ((size_t)t * nk + (c >> 7)) * 8) =
             make_uint2(s_hi, s_lo);
     }
-    alive = route_tokens(p.b, tb, G + 1 + down_tiles, smem, abort_flag);
-  } else {
-    griddep_wait();
-    griddep_launch_dependents();
-    for (int e = threadIdx.x; e <= p.b.E; e += blockDim.x) tb.offsets[e] = p.b.offsets[e];
   }
+  bool alive = route_tokens(p.b, tb, G + 1 + down_tiles, smem, abort_flag);
   __syncthreads();
   if (warp == 0 && alive) build_tile_prefix(p.b, tb, BN);
   // the ring was the routing's scratch: its generic accesses precede the asynchronous copies
-  if (kRoute) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -470,11 +463,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     __syncwarp();
   } else if (warp == 8) {
     // ---------------------------------------------------------------- token rows
-    // The rows of a unit are neighbours (x was split into sorted rows): a stage's come in one box,
-    // its scales in one block.  Only x of the one-launch layer is by token: its rows are gathered
-    // by 16-byte asynchronous copies, 8 lanes a row, into the swizzled tile, the scale words by
-    // 4-byte copies.  Every lane's copies arrive on the stage's barrier by themselves: a warp that
-    // waited for them to land before it announced a stage filled one slot in a copy's latency.
+    // Rows of h are neighbours: a stage's come in one box, its scales in one block.  x is by token:
+    // its rows are gathered by 16-byte asynchronous copies, 8 lanes a row, into the swizzled tile,
+    // the scale words by 4-byte copies.  Every lane's copies arrive on the stage's barrier by
+    // themselves: a warp that waited for them to land before it announced a stage filled one slot
+    // in a copy's latency.
     const int h_target = n_rows * up_tiles * 4;
     bool all_ready = false;
     int st = 0, filled = 0;
@@ -500,16 +493,15 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         fence_proxy_async_global();  // other CTAs' stores, read by TMA
       }
       const int K = up ? d : f, nk = K / 128;
-      if (!kRoute || !up) {
-        const CUtensorMap *m = up ? &p.tm_x : &p.tm_h;
-        const uint8_t *sc = (up ? p.xs : p.hs) + (size_t)w.tile * nk * C::SB_BYTES;
+      if (!up) {
+        const uint8_t *sc = p.hs + (size_t)w.tile * nk * C::SB_BYTES;
         for (int kc = 0; kc < nk; ++kc) {
           ok = warp_wait(&empty[st], ph ^ 1, 35);
           if (!ok) break;
           if (elect_one()) {
-            if (kRowArrivals > 1) mbar_arrive_n(&full[st], kRowArrivals - 1);
+            mbar_arrive_n(&full[st], kRowArrivals - 1);
             mbar_arrive_expect_tx(&full[st], C::B_BYTES + C::SB_BYTES);
-            tma_load_3d(sB + st * C::B_BYTES, m, &full[st], kc * 128, w.row0, 0);
+            tma_load_3d(sB + st * C::B_BYTES, &p.tm_h, &full[st], kc * 128, w.row0, 0);
             bulk_load(sSB + st * C::SB_BYTES, sc + kc * C::SB_BYTES, C::SB_BYTES, &full[st]);
           }
           __syncwarp();
@@ -525,7 +517,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       // This lane's piece of the first 4 rows (hi, then lo) and its scale word: addresses once a
       // unit, so that a unit of one or two tokens -- most are -- takes two copies a stage.
       int my_row = w.row0 + lane;
-      if (lane < w.n) my_row = w.g < p.b.E ? perm[w.row0 + lane] / p.b.k : w.tok0 + lane;
+      if (lane < w.n) my_row = w.g < p.b.E ? tb.perm[w.row0 + lane] / p.b.k : w.tok0 + lane;
       const int c = lane & 7;  // 16-byte chunk of a 128-byte row
       auto piece = [&](int r, uint32_t &to, const uint8_t *&src) {
         const int i = r < w.n ? r : r - w.n, t = r < w.n ? r : BN + i;  // row of the tile
@@ -602,7 +594,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         if (elect_one()) {
           if (there) {
             // gathered token rows: written by the copies' generic proxy, read by the tensor cores
-            if (kRoute) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             tc_cp_scales(sf, sa_base + st * C::SA_BYTES);
             tc_cp_scales(sf + 4, sb_base + st * C::SB_BYTES);
             const uint64_t a = sdesc_k_sw128(a_base + st * C::A_BYTES),
@@ -640,8 +632,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       // down: routed_scale * gate of tokens lane and 32 + lane, asked for before the wait
       float sc0 = 1.f, sc1 = 1.f;
       if (!up && w.g < p.b.E) {
-        if (lane < w.n) sc0 = p.b.routed_scale * gate[perm[w.row0 + lane]];
-        if (BN > 32 && 32 + lane < w.n) sc1 = p.b.routed_scale * gate[perm[w.row0 + 32 + lane]];
+        if (lane < w.n) sc0 = p.b.routed_scale * tb.gate[tb.perm[w.row0 + lane]];
+        if (BN > 32 && 32 + lane < w.n) sc1 = p.b.routed_scale * tb.gate[tb.perm[w.row0 + 32 + lane]];
       }
       alive = warp_wait(&tfull[acc], (it >> 1) & 1, 39);
       if (!alive) break;
@@ -698,7 +690,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     alive = warp_wait(mma_end, 0, 47);
   }
   if (alive && (warp < 4 || warp > 9))
-    combine_pieces(p.b, slot_row, kMxDown, n_rows * 4, warp < 4 ? warp : warp - 6, kMxWarps - 6,
+    combine_pieces(p.b, tb.slot, kMxDown, n_rows * 4, warp < 4 ? warp : warp - 6, kMxWarps - 6,
                    abort_flag);
   tc_fence_before();
   __syncthreads();
@@ -706,7 +698,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
-  if (kRoute && threadIdx.x == 0) leave_grid(p.b);
+  if (threadIdx.x == 0) leave_grid(p.b);
 }
 
 }  // namespace moe

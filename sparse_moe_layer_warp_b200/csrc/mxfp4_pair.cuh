@@ -21,8 +21,9 @@
 namespace moe {
 
 constexpr int kMxPairEpiWarps = 16;  // warps 0-15: four for each TMEM lane quadrant
-// then the leader's MMA, the peer's scheduler; two warps for the weights; token rows.  20 warps: a
-// 21st would leave 80 registers a thread, and the epilogue spilled.
+// then MMA (two warps in the leader: one for each weight tile, as in mxfp4_layer.cuh; the first is the
+// peer's scheduler), weights, token rows.  20 warps: a 21st would leave 80 registers a thread, and
+// the epilogue spilled.
 constexpr int kMxPairThreads = 32 * (kMxPairEpiWarps + 4);
 
 struct MxPairParams {
@@ -42,7 +43,7 @@ struct MxPairCfg {
   static constexpr int SA_BYTES = 2 * kMxScaleBlock, SB_BYTES = scale_block_bytes(BN);
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
   static constexpr int TILE_COLS = 2 * BN, ACC_COLS = 2 * TILE_COLS;
-  static constexpr int SF_COLS = 16;  // weights 2 x 4, tokens 8
+  static constexpr int SF_COLS = 24;  // for each of the two MMA warps: weights 4, tokens 8
   static constexpr int TMEM_COLS = 512;
   static_assert(ACC_COLS + 2 * SF_COLS <= TMEM_COLS && SB_BYTES == 1024, "TMEM");
   static constexpr int FIXED = StreamTables::BYTES + 1024 /*barriers*/ + 1024 /*alignment*/;
@@ -100,16 +101,16 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 3);  // the leader's three producer warps
-      mbar_init(&empty[s], 1);
+      mbar_init(&full[s], 2);  // the leader's two producer warps
+      mbar_init(&empty[s], 2);  // MMA warps
     }
-    mbar_init(tfull, 1);
+    mbar_init(tfull, 2);
     mbar_init(tempty, 2 * kMxPairEpiWarps);
     for (int q = 0; q < kUnitQ; ++q) {
       mbar_init(&uq_full[q], 1);
-      mbar_init(&uq_empty[q], 2 * (kMxPairEpiWarps + 3) + 1);
+      mbar_init(&uq_empty[q], 2 * (kMxPairEpiWarps + 2) + 2);
     }
-    mbar_init(mma_end, 1);
+    mbar_init(mma_end, 2);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_g);
@@ -180,10 +181,8 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
                        return true;
                      });
     __syncwarp();
-  } else if (warp == kMxPairEpiWarps + 1 || warp == kMxPairEpiWarps + 2) {
+  } else if (warp == kMxPairEpiWarps + 2) {
     // ---------------------------------------------------------------- weights
-    // Warp j: tile j of the unit.
-    const int j = __reduce_max_sync(0xffffffffu, warp) - (kMxPairEpiWarps + 1);
     const uint64_t pol_once = policy_evict_first(), pol_reuse = policy_evict_last();
     int st = 0, filled = 0;
     uint32_t ph = 0;
@@ -191,27 +190,28 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     bool ok = true;
     while ((ok = next_unit(w, 45)) && w.kind >= 0) {
       const bool up = w.kind == 0;
-      const int nk = (up ? d : f) / 128, m_rows = up ? f : d;
-      const bool there = tile_row(w, j, rank) < m_rows;
-      const int row = w.g * m_rows + tile_row(w, j, rank);
-      const uint32_t bytes = ((tile_row(w, j, 0) < m_rows) + (tile_row(w, j, 1) < m_rows)) *
-                             (kMxTile * 64 + kMxScaleBlock);  // of both CTAs
-      uint8_t *a = sA + j * (C::A_BYTES / 2), *sa = sSA + j * kMxScaleBlock;
-      const CUtensorMap *m = up ? (j ? &p.tm_u : &p.tm_g) : &p.tm_d;
-      const CUtensorMap *sc = up ? (j ? &p.tm_su : &p.tm_sg) : &p.tm_sd;
+      const int nk = (up ? d : f) / 128, m_rows = up ? f : d, row = w.g * m_rows;
+      const int row_a = tile_row(w, 0, rank), row_b = tile_row(w, 1, rank);
+      int tiles = 0;  // of both CTAs
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tiles += tile_row(w, i >> 1, i & 1) < m_rows;
+      const CUtensorMap *ma = up ? &p.tm_g : &p.tm_d, *mb = up ? &p.tm_u : &p.tm_d;
+      const CUtensorMap *sa = up ? &p.tm_sg : &p.tm_sd, *sb = up ? &p.tm_su : &p.tm_sd;
       const uint64_t pol = w.uses == 1 ? pol_once : pol_reuse;
       for (int kc = 0; kc < nk; ++kc) {
         ok = warp_wait(&empty[st], ph ^ 1, 32);
         if (!ok) break;
         if (elect_one()) {
-          if (leader) {
-            if (bytes) mbar_arrive_expect_tx(&full[st], bytes);
-            else mbar_arrive(&full[st]);
+          const uint32_t bar = full_leader + st * 8;
+          uint8_t *a = sA + st * C::A_BYTES, *s = sSA + st * C::SA_BYTES;
+          if (leader) mbar_arrive_expect_tx(&full[st], tiles * (kMxTile * 64 + kMxScaleBlock));
+          if (row_a < m_rows) {
+            tma_load_2d_pair(a, ma, bar, kc * 128, row + row_a, pol);
+            tma_load_2d_pair(s, sa, bar, 0, (row + row_a) / kMxTile * nk + kc, pol);
           }
-          if (there) {
-            const uint32_t bar = full_leader + st * 8;
-            tma_load_2d_pair(a + st * C::A_BYTES, m, bar, kc * 128, row, pol);
-            tma_load_2d_pair(sa + st * C::SA_BYTES, sc, bar, 0, row / kMxTile * nk + kc, pol);
+          if (row_b < m_rows) {
+            tma_load_2d_pair(a + C::A_BYTES / 2, mb, bar, kc * 128, row + row_b, pol);
+            tma_load_2d_pair(s + kMxScaleBlock, sb, bar, 0, (row + row_b) / kMxTile * nk + kc, pol);
           }
         }
         __syncwarp();
@@ -272,61 +272,58 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     }
     if (!ok && lane == 0 && leader) drain_stages(full, filled, S);
     __syncwarp();
-  } else if (warp == kMxPairEpiWarps) {
+  } else if (warp == kMxPairEpiWarps || warp == kMxPairEpiWarps + 1) {
     // ---------------------------------------------------------------- MMA (leader)
-    int st = 0, it = 0;
-    uint32_t ph = 0;
-    Unit w;
-    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem_base);
-    const uint32_t a_base = smem_u32(sA), b_base = smem_u32(sB), sa_base = smem_u32(sSA),
-                   sb_base = smem_u32(sSB);
-    while (next_unit(w, 36)) {
-      const int kind = w.kind;
-      if (kind < 0) break;
-      const int nk = (kind == 0 ? d : f) / 128;
-      const int half = scale_lo_row(w.n, BN);
-      const bool two = kind == 0 || w.mt * 512 + 256 < d;
-      bool ok = warp_wait(tempty, (it & 1) ^ 1, 46);
-      ++it;
-      tc_fence_after();
-      for (int kc = 0; ok && kc < nk; ++kc) {
-        ok = warp_wait(&full[st], ph, 37);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t sf = tm + C::ACC_COLS + (kc & 1) * C::SF_COLS;
-        const uint32_t sa = sa_base + st * C::SA_BYTES, sb = sb_base + st * C::SB_BYTES;
-        if (elect_one()) {
-          tc_cp_scales_pair(sf, sa);
-          if (two) tc_cp_scales_pair(sf + 4, sa + kMxScaleBlock);
-          tc_cp_scales_pair(sf + 8, sb);
-          if (half > 64) tc_cp_scales_pair(sf + 12, sb + kMxScaleBlock);
-          const uint64_t a = sdesc_k_sw128(a_base + st * C::A_BYTES),
-                         a2 = sdesc_k_sw128(a_base + st * C::A_BYTES + C::A_BYTES / 2),
-                         b = sdesc_k_sw128(b_base + st * C::B_BYTES);
-          const uint32_t id0 = idesc_mx(256, 2 * half);
+    if (leader) {
+      const int j = __reduce_max_sync(0xffffffffu, warp) - kMxPairEpiWarps;
+      int st = 0, it = 0;
+      uint32_t ph = 0;
+      Unit w;
+      const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem_base), d0 = tm + j * C::TILE_COLS;
+      const uint32_t a_base = smem_u32(sA) + j * (C::A_BYTES / 2), b_base = smem_u32(sB),
+                     sa_base = smem_u32(sSA) + j * kMxScaleBlock, sb_base = smem_u32(sSB);
+      while (next_unit(w, 36) && w.kind >= 0) {
+        const int nk = (w.kind == 0 ? d : f) / 128, half = scale_lo_row(w.n, BN);
+        const bool there = tile_row(w, j, 0) < (w.kind == 0 ? f : d);
+        const uint32_t id0 = idesc_mx(256, 2 * half);
+        bool ok = warp_wait(tempty, (it & 1) ^ 1, 46), ready = false;
+        ++it;
+        for (int kc = 0; ok && kc < nk; ++kc) {
+          if (!__all_sync(0xffffffffu, ready)) ok = warp_wait(&full[st], ph, 37);
+          if (!ok) break;
+          tc_fence_after();
+          const int st1 = st + 1 == S ? 0 : st + 1;
+          const uint32_t ph1 = st + 1 == S ? ph ^ 1 : ph;
+          ready = kc + 1 < nk && mbar_test_wait(&full[st1], ph1);
+          const uint32_t sf = tm + C::ACC_COLS + (kc & 1) * C::SF_COLS + j * (C::SF_COLS / 2);
+          if (elect_one()) {
+            if (there) {
+              const uint32_t sb = sb_base + st * C::SB_BYTES;
+              tc_cp_scales_pair(sf, sa_base + st * C::SA_BYTES);
+              tc_cp_scales_pair(sf + 4, sb);
+              if (half > 64) tc_cp_scales_pair(sf + 8, sb + kMxScaleBlock);
+              const uint64_t a = sdesc_k_sw128(a_base + st * C::A_BYTES),
+                             b = sdesc_k_sw128(b_base + st * C::B_BYTES);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t id = id0 | ((uint32_t)kk << 4) | ((uint32_t)kk << 29);
-            const uint32_t add = (kc | kk) ? 1u : 0u;
-            tc_mma_mx_pair(tm, a + 2 * kk, b + 2 * kk, id, sf, sf + 8, add);
-            if (two) tc_mma_mx_pair(tm + C::TILE_COLS, a2 + 2 * kk, b + 2 * kk, id, sf + 4,
-                                    sf + 8, add);
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_mx_pair(d0, a + 2 * kk, b + 2 * kk,
+                               id0 | ((uint32_t)kk << 4) | ((uint32_t)kk << 29), sf, sf + 4,
+                               (kc | kk) ? 1u : 0u);
+            }
+            tc_commit_pair_both(&empty[st]);
+            if (kc == nk - 1) tc_commit_pair_both(tfull);
           }
-          tc_commit_pair_both(&empty[st]);
-          if (kc == nk - 1) tc_commit_pair_both(tfull);
+          __syncwarp();
+          st = st1;
+          ph = ph1;
         }
-        __syncwarp();
-        if (++st == S) {
-          st = 0;
-          ph ^= 1;
-        }
+        if (!ok) break;
       }
-      if (!ok) break;
-    }
-    if (lane == 0) {
-      tc_commit_pair_local(mma_end);
-      volatile int no_abort = 0;
-      mbar_wait_bounded(mma_end, 0, &no_abort, nullptr, 0);
+      if (lane == 0) {
+        tc_commit_pair_local(mma_end);
+        volatile int no_abort = 0;
+        mbar_wait_bounded(mma_end, 0, &no_abort, nullptr, 0);
+      }
     }
     __syncwarp();
   } else if (warp < kMxPairEpiWarps) {

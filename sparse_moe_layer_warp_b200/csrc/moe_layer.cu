@@ -8,6 +8,9 @@
 //         (small token tiles: the up GEMM gathers the rows of x itself)
 //   fp32: SIMT up+SwiGLU -> SIMT down                                    (expert_simt.cuh)
 //   -> gate-weighted combine                                             (expert_simt.cuh)
+// MXFP4 experts, up to 64 tokens: all of it in one launch             (mxfp4_layer.cuh)
+// MXFP4 experts, more: routing -> split rows -> experts -> combine     (mxfp4_pair.cuh)
+// (moe_forward_few: bf16 in one launch, weight_stream.cuh)
 // (decode-sized batches: routing in one launch; large groups: CTA-pair GEMMs,
 // grouped_gemm_pair.cuh).  One call of moe_backward (bf16) launches:
 //   the forward's routing -> row bookkeeping, padded offsets, padded sorted rows
@@ -77,7 +80,7 @@ struct moe_layer {
   // MXFP4 expert weights (moe_layer_init_mxfp4): w holds the codes, these the scales
   int mx, mx_pair_grid;
   const uint8_t *sc_gate, *sc_up, *sc_down;
-  // the expert weights as the weight-streaming kernel loads them (bf16 or code bytes)
+  // the expert weights as the one-launch and MXFP4 kernels load them (bf16 or codes)
   CUtensorMap tm_st_g, tm_st_u, tm_st_d;
 };
 
@@ -1501,9 +1504,6 @@ StreamBase stream_base(const moe_layer *L, const void *x, int T, void *out, void
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.y = at<float>(ws, W.y);
   p.offsets = at<int>(ws, W.offsets);
-  p.perm = at<int>(ws, W.perm);
-  p.slot_row = at<int>(ws, W.slot_row);
-  p.gate = at<float>(ws, W.gate);
   p.w_router = static_cast<const __nv_bfloat16 *>(L->w.w_router);
   p.bias = L->w.router_bias;
   p.logits = at<float>(ws, W.logits);

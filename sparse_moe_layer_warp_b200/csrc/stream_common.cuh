@@ -1,6 +1,7 @@
-// stream_common.cuh -- what the persistent whole-layer kernels share (weight_stream.cuh for bf16
-// weights, mxfp4_layer.cuh for MXFP4): routing inside the kernel, the work units and their
-// scheduler, the combine, suspended waits.
+// stream_common.cuh -- what the persistent whole-layer kernels share (weight_stream.cuh: one launch,
+// bf16 weights; mxfp4_layer.cuh: one launch, MXFP4 weights; mxfp4_pair.cuh: the experts of many
+// tokens, MXFP4 weights): routing inside the kernel, the work units and their scheduler, the
+// combine, suspended waits.
 //
 //   up    h[r, c]  = silu(x_r . W_g[e, c]) * (x_r . W_u[e, c])      row r of the sorted space
 //   down  y[r, c]  = scale_r * (h_r . W_d[e, c])       scale_r = routed_scale * gate, shared 1
@@ -14,8 +15,8 @@
 // down units.
 //
 // Waiting: a down unit's token rows wait for counts of finished h rows, the combine for counts of
-// finished y rows.  A unit is only ever claimed by a CTA that runs, and finishing it waits for
-// up units alone (claimed before), so these waits end whatever the residency of the grid.  The
+// finished y rows.  A unit is only ever claimed by a CTA (or pair) that runs, and finishing it waits
+// for up units alone (claimed before), so these waits end whatever the residency of the grid.  The
 // one-launch layer adds one barrier of the grid after the router's logits, so it is a cooperative
 // launch.  All waits are bounded.
 #pragma once
@@ -42,8 +43,7 @@ struct StreamBase {
   const __nv_bfloat16 *x;                  // [T, d]
   __nv_bfloat16 *out;                      // [T, d]
   float *y;                                // [P, d]
-  const int *offsets, *perm, *slot_row;    // routing (one-launch layer: made by the kernel itself)
-  const float *gate;
+  const int *offsets;                      // CTA pairs: [E + 1], from the routing kernels
   const __nv_bfloat16 *w_router;           // one-launch layer
   const float *bias;
   float *logits;                           // [T, E]

@@ -1581,9 +1581,9 @@ moe_status launch_mx_pair(const moe_layer *L, const void *x, int T, void *out, v
             encode_scale_blocks(&p.tm_xs, at<uint8_t>(ws, W.x_scale),
                                 tiles * 2 * (c.d_model / 128), 2) &&
             encode_scale_blocks(&p.tm_hs, p.hs, tiles * 2 * (c.d_ff / 128), 2);
-  for (int i = 0; i < 2; ++i)
-    ok = ok && encode_u8_2d(&p.tm_x[i], xs, c.d_model, 2 * P, 56u << i) &&
-         encode_u8_2d(&p.tm_h[i], p.h.hi, c.d_ff, 2 * P, 56u << i);
+  for (int i = 0; i < 3; ++i)
+    ok = ok && encode_u8_2d(&p.tm_x[i], xs, c.d_model, 2 * P, pair_box(i)) &&
+         encode_u8_2d(&p.tm_h[i], p.h.hi, c.d_ff, 2 * P, pair_box(i));
   if (!ok) return MOE_ERR_CUDA;
   return launch_cl(mxfp4_pair_kernel, dim3(L->mx_pair_grid), dim3(kMxPairThreads), MxPairCfg::SMEM,
                    st, 2, p);
@@ -1635,8 +1635,8 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
                                  at<int>(ws, W.slot_row), at<int>(ws, W.chunk_hist), reset,
                                  st)) != MOE_OK ||
       (s = launch(split_rows_kernel,
-                  dim3(grid_for((size_t)T, 8, L->num_sms)), dim3(256), 0, st,
-                  static_cast<const __nv_bfloat16 *>(x), at<int>(ws, W.slot_row),
+                  dim3(grid_for((size_t)T * ((c.d_model + 511) / 512), 8, L->num_sms)), dim3(256), 0,
+                  st, static_cast<const __nv_bfloat16 *>(x), at<int>(ws, W.slot_row),
                   at<int>(ws, W.idx), at<int>(ws, W.offsets), T, c.d_model, c.n_experts, c.top_k,
                   c.n_shared, kMxPairBN,
                   split_rows(at<uint8_t>(ws, W.x_split), P, c.d_model),
@@ -1822,8 +1822,8 @@ static bool mxfp4_args(const void *m, moe_dtype dtype, long long rows, int cols,
   return aligned16(m) && aligned16(codes);
 }
 
-static dim3 mxfp4_grid(size_t lanes) {  // 256 threads; enough blocks to fill the device
-  const size_t b = (lanes + 255) / 256;
+static dim3 mxfp4_grid(size_t pieces, int unroll) {  // 256 threads; enough blocks to fill the device
+  const size_t b = (pieces + 256 * unroll - 1) / (256 * unroll);
   return dim3((unsigned)(b < 148 * 8 ? b : 148 * 8));
 }
 
@@ -1834,9 +1834,9 @@ moe_status moe_mxfp4_quantize(const void *src, moe_dtype dtype, long long rows, 
   const size_t lanes = (size_t)rows * cols / kMxPerLane;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == MOE_BF16)
-    return launch(mxfp4_quantize_kernel<__nv_bfloat16>, mxfp4_grid(lanes), dim3(256), 0, st,
+    return launch(mxfp4_quantize_kernel<__nv_bfloat16>, mxfp4_grid(lanes, kMxUnroll), dim3(256), 0, st,
                   static_cast<const __nv_bfloat16 *>(src), lanes, codes, scales);
-  return launch(mxfp4_quantize_kernel<float>, mxfp4_grid(lanes), dim3(256), 0, st,
+  return launch(mxfp4_quantize_kernel<float>, mxfp4_grid(lanes, kMxUnroll), dim3(256), 0, st,
                 static_cast<const float *>(src), lanes, codes, scales);
 }
 
@@ -1847,9 +1847,9 @@ moe_status moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, lon
   const size_t lanes = (size_t)rows * cols / kMxPerLane;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == MOE_BF16)
-    return launch(mxfp4_dequantize_kernel<__nv_bfloat16>, mxfp4_grid(lanes), dim3(256), 0, st,
+    return launch(mxfp4_dequantize_kernel<__nv_bfloat16>, mxfp4_grid(lanes, kMxUnroll), dim3(256), 0, st,
                   codes, scales, lanes, static_cast<__nv_bfloat16 *>(dst));
-  return launch(mxfp4_dequantize_kernel<float>, mxfp4_grid(lanes), dim3(256), 0, st, codes,
+  return launch(mxfp4_dequantize_kernel<float>, mxfp4_grid(lanes, kMxUnroll), dim3(256), 0, st, codes,
                 scales, lanes, static_cast<float *>(dst));
 }
 
@@ -1860,7 +1860,7 @@ moe_status moe_mxfp4_tile_scales(const uint8_t *scales, long long rows, int cols
   if (!scales || !tiled || rows > (1ll << 62) / cols) return MOE_ERR_INVALID_ARG;
   if (!aligned16(scales) || !aligned16(tiled)) return MOE_ERR_ALIGNMENT;
   const size_t words = (size_t)rows * (cols / 128);
-  return launch(mxfp4_tile_scales_kernel, mxfp4_grid(words), dim3(256), 0,
+  return launch(mxfp4_tile_scales_kernel, mxfp4_grid(words, 1), dim3(256), 0,
                 static_cast<cudaStream_t>(stream), reinterpret_cast<const uint32_t *>(scales), words,
                 cols / 128, reinterpret_cast<uint32_t *>(tiled));
 }

@@ -17,6 +17,7 @@
 namespace moe {
 
 constexpr int kMxBlock = 32;   // values that share a scale
+constexpr int kMxUnroll = 4;   // pieces of 8 values a thread takes at a time, 256 apart
 constexpr int kMxPerLane = 8;  // values a lane converts: four lanes hold a block
 
 // 2^(byte - 127): byte 0 is fp32's subnormal 2^-127, byte 255 NaN
@@ -84,32 +85,44 @@ __device__ __forceinline__ uint32_t block_amax_bits(const float (&v)[8]) {
 // value of v / 2^s, ties to the even code, magnitudes past 6 saturate to 6.  v / 2^s is exact: a
 // product with a power of two (only results far below the smallest code lose bits).  A block that
 // holds an infinity or a NaN becomes NaN: byte 255, codes 0.
-// One pass, 16 or 32 bytes read a lane, four lanes a block; bound by HBM.
+// One pass, 16 or 32 bytes read a lane, four lanes a block, kMxUnroll loads in flight a thread; bound
+// by HBM.
 template <typename Tin>
 __global__ void __launch_bounds__(256)
     mxfp4_quantize_kernel(const Tin *__restrict__ src, size_t n_lanes, uint8_t *__restrict__ codes,
                           uint8_t *__restrict__ scales) {
   griddep_wait();
   griddep_launch_dependents();
-  const size_t step = (size_t)gridDim.x * blockDim.x;
-  const size_t n_round = (n_lanes + 31) & ~(size_t)31;  // whole warps take part in the shuffles
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n_round; i += step) {
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (i < n_lanes) load8(src + i * kMxPerLane, v);
-    const uint32_t field = block_amax_bits(v) >> 23;
-    const uint32_t byte = field == 255u ? 255u : (field > 2u ? field - 2u : 0u);
-    const float inv = byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
-    uint32_t c = 0;
-    if (byte != 255u) {
+  const size_t step = (size_t)gridDim.x * 256 * kMxUnroll;
+  // whole warps take part in the shuffles
+  for (size_t i0 = (size_t)blockIdx.x * 256 * kMxUnroll; i0 < n_lanes; i0 += step) {
+    float v[kMxUnroll][8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        c |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[2 * j] * inv, v[2 * j + 1] * inv),
-                                                __NV_E2M1, cudaRoundNearest)
-             << (8 * j);
+    for (int u = 0; u < kMxUnroll; ++u) {
+      const size_t i = i0 + u * 256 + threadIdx.x;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
+      if (i < n_lanes) load8(src + i * kMxPerLane, v[u]);
     }
-    if (i < n_lanes) {
-      *reinterpret_cast<uint32_t *>(codes + i * 4) = c;
-      if ((i & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+#pragma unroll
+    for (int u = 0; u < kMxUnroll; ++u) {
+      const size_t i = i0 + u * 256 + threadIdx.x;
+      const uint32_t field = block_amax_bits(v[u]) >> 23;
+      const uint32_t byte = field == 255u ? 255u : (field > 2u ? field - 2u : 0u);
+      const float inv = byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
+      uint32_t c = 0;
+      if (byte != 255u) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          c |= (uint32_t)__nv_cvt_float2_to_fp4x2(
+                   make_float2(v[u][2 * j] * inv, v[u][2 * j + 1] * inv), __NV_E2M1,
+                   cudaRoundNearest)
+               << (8 * j);
+      }
+      if (i < n_lanes) {
+        *reinterpret_cast<uint32_t *>(codes + i * 4) = c;
+        if ((i & 3) == 0) scales[i >> 2] = (uint8_t)byte;
+      }
     }
   }
 }
@@ -122,19 +135,30 @@ __global__ void __launch_bounds__(256)
                             size_t n_lanes, Tout *__restrict__ dst) {
   griddep_wait();
   griddep_launch_dependents();
-  const size_t step = (size_t)gridDim.x * blockDim.x;
-  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n_lanes; i += step) {
-    uint32_t h[4];
-    e2m1x8_to_half(*reinterpret_cast<const uint32_t *>(codes + i * 4), h);
-    const float s = e8m0_to_f32(scales[i >> 2]);
-    float v[8];
+  const size_t step = (size_t)gridDim.x * 256 * kMxUnroll;
+  for (size_t i0 = (size_t)blockIdx.x * 256 * kMxUnroll; i0 < n_lanes; i0 += step) {
+    uint32_t c[kMxUnroll], b[kMxUnroll];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
-      v[2 * j] = f.x * s;
-      v[2 * j + 1] = f.y * s;
+    for (int u = 0; u < kMxUnroll; ++u) {
+      const size_t i = i0 + u * 256 + threadIdx.x;
+      c[u] = i < n_lanes ? *reinterpret_cast<const uint32_t *>(codes + i * 4) : 0u;
+      b[u] = i < n_lanes ? scales[i >> 2] : 0u;
     }
-    store8(dst + i * kMxPerLane, v);
+#pragma unroll
+    for (int u = 0; u < kMxUnroll; ++u) {
+      const size_t i = i0 + u * 256 + threadIdx.x;
+      uint32_t h[4];
+      e2m1x8_to_half(c[u], h);
+      const float s = e8m0_to_f32(b[u]);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+        v[2 * j] = f.x * s;
+        v[2 * j + 1] = f.y * s;
+      }
+      if (i < n_lanes) store8(dst + i * kMxPerLane, v);
+    }
   }
 }
 

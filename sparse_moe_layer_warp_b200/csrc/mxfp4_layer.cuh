@@ -251,16 +251,23 @@ __device__ __forceinline__ void store_h_chunk(const SplitRows &h, uint8_t *hs, i
 }
 
 // x [T, d] -> the split rows of the sorted space with their scale blocks: token t to its k routed
-// rows and its shared row.  One warp a token: converts 512 columns at a time and stores them
-// k + n_shared times; bound by HBM (2 d bytes read, 2 d (k + n_shared) written a token).
+// rows and its shared row.  One warp converts 512 columns of a token and stores them k + n_shared
+// times; bound by HBM (2 d bytes read, 2 d (k + n_shared) written a token).
 __global__ void __launch_bounds__(256)
     split_rows_kernel(const __nv_bfloat16 *__restrict__ x, const int *__restrict__ slot_row,
                       const int *__restrict__ idx, const int *__restrict__ offsets, int T, int d,
                       int E, int k, int n_shared, int BN, SplitRows out, uint8_t *xs) {
+  const int lane = threadIdx.x & 31, nk = d / 128, n_warps = gridDim.x * 8;
+  const int chunks = (d + 511) / 512;
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, nk = d / 128, n_warps = gridDim.x * 8;
-  for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += n_warps) {
+  for (long long item = blockIdx.x * 8 + (threadIdx.x >> 5); item < (long long)T * chunks;
+       item += n_warps) {
+    const int t = (int)(item / chunks), c = (int)(item % chunks) * 512 + lane * 16;
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    if (c < d) load16(x + (size_t)t * d + c, v);
     // lane j: row of slot j, its tile's number, its hi and lo rows in a block; the shared row (all 32
     // lanes may have slots) beside them
     auto place = [&](int g, int off, int rows, int row, int &tile, int &r, int &r_lo) {
@@ -275,29 +282,22 @@ __global__ void __launch_bounds__(256)
       place(g, off, offsets[g + 1] - off, row, tile, r, r_lo);
     }
     place(E, T * k, T, T * k + t, s_tile, s_r, s_lo);
-    for (int c0 = 0; c0 < d; c0 += 512) {
-      const int c = c0 + lane * 16;
-      float v[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.f;
-      if (c < d) load16(x + (size_t)t * d + c, v);
-      uint4 hi, lo;
-      uint32_t w_hi, w_lo;  // scale words
-      split_lane(v, hi, lo, w_hi, w_lo);
-      for (int j = 0; j < k + n_shared; ++j) {
-        const bool slot = j < k;
-        const size_t rw = slot ? __shfl_sync(0xffffffffu, row, j) : T * k + t;
-        const size_t tl = slot ? __shfl_sync(0xffffffffu, tile, j) : s_tile;
-        const int rj = slot ? __shfl_sync(0xffffffffu, r, j) : s_r;
-        const int lj = slot ? __shfl_sync(0xffffffffu, r_lo, j) : s_lo;
-        if (c >= d) continue;
-        *reinterpret_cast<uint4 *>(out.hi + rw * d + c) = hi;
-        *reinterpret_cast<uint4 *>(out.lo + rw * d + c) = lo;
-        if ((lane & 7) < 2)
-          *reinterpret_cast<uint32_t *>(xs + (tl * nk + (c >> 7)) * scale_block_bytes(BN) +
-                                        scale_row_at((lane & 1) ? lj : rj)) =
-              (lane & 1) ? w_lo : w_hi;
-      }
+    uint4 hi, lo;
+    uint32_t w_hi, w_lo;  // scale words
+    split_lane(v, hi, lo, w_hi, w_lo);
+    for (int j = 0; j < k + n_shared; ++j) {
+      const bool slot = j < k;
+      const size_t rw = slot ? __shfl_sync(0xffffffffu, row, j) : T * k + t;
+      const size_t tl = slot ? __shfl_sync(0xffffffffu, tile, j) : s_tile;
+      const int rj = slot ? __shfl_sync(0xffffffffu, r, j) : s_r;
+      const int lj = slot ? __shfl_sync(0xffffffffu, r_lo, j) : s_lo;
+      if (c >= d) continue;
+      *reinterpret_cast<uint4 *>(out.hi + rw * d + c) = hi;
+      *reinterpret_cast<uint4 *>(out.lo + rw * d + c) = lo;
+      if ((lane & 7) < 2)
+        *reinterpret_cast<uint32_t *>(xs + (tl * nk + (c >> 7)) * scale_block_bytes(BN) +
+                                      scale_row_at((lane & 1) ? lj : rj)) =
+            (lane & 1) ? w_lo : w_hi;
     }
   }
 }

@@ -30,11 +30,14 @@ struct MxPairParams {
   StreamBase b;
   CUtensorMap tm_g, tm_u, tm_d;      // codes, box {128, 128}, padded 4-bit
   CUtensorMap tm_sg, tm_su, tm_sd;   // their scale blocks as words, box {128, 1}
-  CUtensorMap tm_x[2], tm_h[2];      // token rows, hi then lo [2 P, cols]: box 56 or 112 rows
+  CUtensorMap tm_x[3], tm_h[3];      // token rows, hi then lo [2 P, cols]: boxes of pair_box rows
   CUtensorMap tm_xs, tm_hs;          // scale blocks as words, box {128, 2}
   SplitRows h;
   uint8_t *hs;
 };
+
+// Rows of the three token boxes: a tile of few tokens loads few rows.
+__host__ __device__ constexpr int pair_box(int i) { return i == 0 ? 16 : (i == 1 ? 56 : kMxPairBN); }
 
 struct MxPairCfg {
   static constexpr int BN = kMxPairBN;
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         __syncwarp();  // the elected lane's copies follow those two loads
         fence_proxy_async_global();  // other CTAs' stores, read by TMA
       }
-      const int nk = (up ? d : f) / 128, box = w.n > 56 ? 1 : 0;
+      const int nk = (up ? d : f) / 128, box = w.n <= pair_box(0) ? 0 : (w.n <= pair_box(1) ? 1 : 2);
       const CUtensorMap *m = up ? &p.tm_x[box] : &p.tm_h[box], *sc = up ? &p.tm_xs : &p.tm_hs;
       for (int kc = 0; kc < nk; ++kc) {
         ok = warp_wait(&empty[st], ph ^ 1, 35);
@@ -256,7 +259,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         if (elect_one()) {
           const uint32_t bar = full_leader + st * 8;
           if (leader)
-            mbar_arrive_expect_tx(&full[st], 2 * ((box ? 112 : 56) * 128 + C::SB_BYTES));
+            mbar_arrive_expect_tx(&full[st], 2 * (pair_box(box) * 128 + C::SB_BYTES));
           tma_load_2d_pair(sB + st * C::B_BYTES, m, bar, kc * 128, (int)rank * n_rows + w.row0,
                            pol);
           tma_load_2d_pair(sSB + st * C::SB_BYTES, sc, bar, 0, (w.tile * nk + kc) * 2, pol);

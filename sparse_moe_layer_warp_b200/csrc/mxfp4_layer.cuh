@@ -374,9 +374,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
             make_uint2(s_hi, s_lo);
     }
   }
-  bool alive = route_tokens(p.b, tb, G + 1 + down_tiles, smem, abort_flag);
-  __syncthreads();
-  if (warp == 0 && alive) build_tile_prefix(p.b, tb, BN);
+  bool alive = route_tokens(p.b, tb, BN, G + 1 + down_tiles, smem, abort_flag);
   // the ring was the routing's scratch: its generic accesses precede the asynchronous copies
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   tc_fence_before();

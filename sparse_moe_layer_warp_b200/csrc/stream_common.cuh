@@ -200,9 +200,11 @@ constexpr int kRouteScratch =
 // Routing of the one-launch layer, by the whole CTA (16 warps or more).  Zeroes the counters,
 // computes the router's logits of two experts a CTA (the decode routing kernel's sums, so the
 // selection is moe_route's), meets the other CTAs, then selects for all tokens itself: no second
-// barrier.  False when the barrier gave up.
-__device__ __forceinline__ bool route_tokens(const StreamBase &p, const StreamTables &tb, int n_done,
-                                             void *scratch, volatile int *abort_flag) {
+// barrier.  Fills the tables, tile_prefix for token tiles of bt rows among them.  False when the
+// barrier gave up.
+__device__ __forceinline__ bool route_tokens(const StreamBase &p, const StreamTables &tb, int bt,
+                                             int n_done, void *scratch,
+                                             volatile int *abort_flag) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_warps = blockDim.x >> 5;
   const int n_thr = gridDim.x * blockDim.x, thr = blockIdx.x * blockDim.x + threadIdx.x;
   for (int i = thr; i < n_done; i += n_thr) p.done[i] = 0;  // done, done_all, tile_done
@@ -240,8 +242,24 @@ __device__ __forceinline__ bool route_tokens(const StreamBase &p, const StreamTa
     }
   }
   __syncthreads();
+  // one scan of rows (low half) and token tiles (high half): both sums stay below 2^10
+  static_assert(kStreamMaxPairs < 65536, "halves of a word");
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x)
+    hist[e] |= (hist[e] + bt - 1) / bt << 16;
+  __syncthreads();
   block_exclusive_scan(hist, tb.offsets, p.E, warp_sum);
-  if (threadIdx.x == 0) tb.offsets[p.E] = p.T * p.k;
+  const int s_tiles = p.n_shared ? (p.T + bt - 1) / bt : 0;  // the shared expert's come first
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+    const int both = tb.offsets[e];
+    tb.offsets[e] = both & 0xffff;
+    tb.tile_prefix[e + p.n_shared] = (both >> 16) + s_tiles;
+    if (e == p.E - 1) {
+      tb.offsets[p.E] = p.T * p.k;
+      tb.tile_prefix[p.E + p.n_shared] = ((both + hist[e]) >> 16) + s_tiles;
+      if (p.n_shared) tb.tile_prefix[0] = 0;
+    }
+  }
+  __syncthreads();
   for (int q = threadIdx.x; q < p.T * p.k; q += blockDim.x) {
     const int t = q / p.k, e = s_idx[q];
     int rank = __popc(bits[2 * e + (t >> 5)] & ((1u << (t & 31)) - 1u));
@@ -260,7 +278,7 @@ __device__ __forceinline__ int group_rows(const StreamBase &p, const StreamTable
   return g < p.E ? tb.offsets[g + 1] - tb.offsets[g] : p.T;
 }
 
-// tile_prefix for token tiles of bt rows, by one warp.
+// tile_prefix for token tiles of bt rows from the offsets, by one warp.
 __device__ __forceinline__ void build_tile_prefix(const StreamBase &p, const StreamTables &tb,
                                                   int bt) {
   const int lane = threadIdx.x & 31, G = p.E + p.n_shared;

@@ -134,9 +134,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     tma_prefetch_desc(&p.tm_d);
   }
   __syncthreads();  // the abort flag is clear
-  bool alive = route_tokens(p.b, tb, G + 1 + down_tiles, smem, abort_flag);
-  __syncthreads();
-  if (warp == 0 && alive) build_tile_prefix(p.b, tb, BT);
+  bool alive = route_tokens(p.b, tb, BT, G + 1 + down_tiles, smem, abort_flag);
   // the ring was the routing's scratch: its generic accesses precede the asynchronous copies
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();

@@ -1934,7 +1934,7 @@ moe_status moe_forward_partial(moe_handle h, const void *x, int n_tokens, const 
   moe_status s = check_call(h, n_tokens, ws, ws_bytes);
   if (s != MOE_OK) return s;
   const moe_config &c = h->cfg;
-  if (c.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (c.dtype != MOE_BF16 || h->mx) return MOE_ERR_UNSUPPORTED;  // MXFP4: no slices
   if (expert_begin < h->e0 || expert_end < expert_begin || expert_end > h->e1)
     return MOE_ERR_INVALID_ARG;
   if (expert_end - expert_begin + c.top_k > kMaxExperts) return MOE_ERR_UNSUPPORTED;

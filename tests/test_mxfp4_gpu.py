@@ -409,12 +409,25 @@ def test_refusals(cuda_ok):
         assert layer.forward_few(c.x[:0].contiguous()).shape == (0, 256)
     with pytest.raises(MoEError):
         mx.backward(c.x, c.x)                           # serving only
+    # calls that read bf16 weights, with arguments that a bf16 handle takes
+    f32 = torch.empty(65, 256, device="cuda")
+    big = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    for call in (
+        lambda: binding.moe_forward_partial(mx.handle, c.x, 65, None, None, 0, 16, 0, 65, f32, big),
+        lambda: binding.moe_forward_save(mx.handle, c.x, 65, torch.empty_like(c.x),
+                                         big.view(torch.float32), big),
+        lambda: mx.expert_health(65),
+    ):
+        with pytest.raises(MoEError) as e:
+            call()
+        assert e.value.status == binding.MOE_ERR_UNSUPPORTED
     wide = Case(T=17, d=256, E=40, k=32, f=128)         # 544 pairs
     with pytest.raises(MoEError):
         wide.layer(False).forward_few(wide.x)
-    f32 = MoELayer(c.router.float(), c.bias, *(w.float() for w in c.bf16), top_k=4, max_tokens=4)
+    single = MoELayer(c.router.float(), c.bias, *(w.float() for w in c.bf16), top_k=4,
+                      max_tokens=4)
     with pytest.raises(MoEError):
-        f32.forward_few(c.x[:4].float())
+        single.forward_few(c.x[:4].float())
     lib = binding.load_library()
     x, out = c.x[:4].contiguous(), torch.empty_like(c.x[:4])
     ws = mx.workspace(4)

@@ -539,20 +539,20 @@ class MoELayer:
     def set_option(self, option: int, value: int) -> None:
         moe_set_option(self.handle, option, value)
 
-    def workspace(self, n_tokens: int):
+    def workspace(self, n_tokens: int, stream=None):
         need = self.ws_need.get(n_tokens)
         if need is None:
             need = self.ws_need[n_tokens] = moe_workspace_size(self.handle, n_tokens)
         if self.ws is None or self.ws.numel() < need:
             self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            moe_workspace_init(self.handle, self.ws)
+            moe_workspace_init(self.handle, self.ws, stream)  # before the first call that uses it
         return self.ws
 
     def forward(self, x, out=None, stream=None):
         T = self._rows(x)
         out = torch.empty_like(x) if out is None else out
         _expect(out, x.shape, x.dtype, "out")
-        moe_forward(self.handle, x, T, out, self.workspace(T), stream)
+        moe_forward(self.handle, x, T, out, self.workspace(T, stream), stream)
         return out
 
     def forward_few(self, x, out=None, stream=None):
@@ -560,7 +560,7 @@ class MoELayer:
         T = self._rows(x)
         out = torch.empty_like(x) if out is None else out
         _expect(out, x.shape, x.dtype, "out")
-        moe_forward_few(self.handle, x, T, out, self.workspace(T), stream)
+        moe_forward_few(self.handle, x, T, out, self.workspace(T, stream), stream)
         return out
 
     def to_mxfp4(self, max_tokens: int | None = None) -> "MoELayerMXFP4":
@@ -737,6 +737,7 @@ class MoELayerMXFP4(MoELayer):
                 t = torch.empty_like(scales)
                 moe_mxfp4_tile_scales(scales, t)
                 tiled.append((codes, t))
+            torch.cuda.current_stream().synchronize()  # calls may come on any stream
         self.tensors = (w_router, router_bias, *tiled)
         self.handle = moe_layer_init_mxfp4(self.cfg, *self.tensors)
         self.device = w_router.device

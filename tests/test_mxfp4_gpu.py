@@ -287,6 +287,21 @@ def test_two_calls_at_once(cuda_ok, T1, T2):
     assert la.device_status() == 0 and lb.device_status() == 0
 
 
+@pytest.mark.parametrize("T", [1, 40, 200])
+def test_first_call_on_another_stream(cuda_ok, T):
+    """The layer's tables and its workspace are ready for whichever stream calls first."""
+    c = Case(T=T, d=1024, E=64, k=4, f=512)
+    want = c.layer(True).forward(c.x).clone()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    out = torch.empty_like(c.x)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        c.layer(True).forward(c.x, out=out, stream=s)
+        s.synchronize()
+        assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("T", [6, 90, 400])
 def test_not_a_number_stays_with_its_tokens(cuda_ok, T):
     """A block of NaN in one expert, and an infinity in one token: the tokens that meet them become

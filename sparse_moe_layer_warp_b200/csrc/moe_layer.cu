@@ -78,7 +78,7 @@ struct moe_layer {
   cudaStream_t side;
   cudaEvent_t ev_fork, ev_join;
   // MXFP4 expert weights (moe_layer_init_mxfp4): w holds the codes, these the scales
-  int mx, mx_pair_grid;
+  int mx, mx_pair_grid[2];  // CTAs of the pair kernels with tiles of 32 and of 112 tokens
   const uint8_t *sc_gate, *sc_up, *sc_down;
   // the expert weights as the one-launch and MXFP4 kernels load them (bf16 or codes)
   CUtensorMap tm_st_g, tm_st_u, tm_st_d;
@@ -269,9 +269,16 @@ bool few_shape(const moe_config &c, int T) {
   return decode_route_ok(c, T) && T <= kStreamMaxT && T * c.top_k <= kStreamMaxPairs;
 }
 
-// Token rows of a tile of the MXFP4 layer.
+// Token rows of a tile of the MXFP4 layer, by the mean rows of an expert: a smaller tile leaves room
+// for more stages of weights in flight, a larger one reads weights again less often.  At 288 experts,
+// top-8, us: CTA pairs with 32 / 112 rows: 481 / 529 at 256 tokens, 500 / 543 at 384, 522 / 557 at
+// 512, 578 / 600 at 768; with skewed routing 246 / 240 at 256, 348 / 313 at 512.  One launch with 8 /
+// 16 / 32: 175 / 182 / 186 at 16 tokens, 383 / 396 / 399 at 64; 32 experts and 64 tokens 180 / 176 /
+// 184; 8 experts and 32 tokens 107 / 101 / 98.
 int mx_token_tile(const moe_config &c, int T) {
-  return !few_shape(c, T) ? kMxPairBN : T <= 8 ? 8 : T <= 16 ? 16 : 32;
+  const long long pairs = (long long)T * c.top_k, E = c.n_experts;
+  if (!few_shape(c, T)) return pairs <= 12 * E ? 32 : 112;
+  return T <= 8 || pairs <= 4 * E ? 8 : T <= 16 || pairs <= 16 * E ? 16 : 32;
 }
 
 // mx: an MXFP4 handle's layout (x and h as pairs of e4m3 values with their scales; x by token for
@@ -842,9 +849,11 @@ static moe_status layer_init(const moe_config *cfg, const moe_weights *w, int e0
     const uint64_t G = (uint64_t)(e1 - e0) + c.n_shared;  // weight groups held
     if (mx) {
       L->mx = 1;
-      L->mx_pair_grid =
-          cluster_grid_size(mxfp4_pair_kernel, MxPairCfg::SMEM, kMxPairThreads, L);
-      if (L->mx_pair_grid < 2) {
+      L->mx_pair_grid[0] =
+          cluster_grid_size(mxfp4_pair_kernel<32>, MxPairCfg<32>::SMEM, kMxPairThreads, L);
+      L->mx_pair_grid[1] =
+          cluster_grid_size(mxfp4_pair_kernel<112>, MxPairCfg<112>::SMEM, kMxPairThreads, L);
+      if (L->mx_pair_grid[0] < 2 || L->mx_pair_grid[1] < 2) {
         free(L);
         return MOE_ERR_CUDA;
       }
@@ -1560,12 +1569,14 @@ bool encode_scale_blocks(CUtensorMap *m, const void *base, uint64_t n, uint32_t 
          CUDA_SUCCESS;
 }
 
-// MXFP4 layer on CTA pairs.
+// The experts of the MXFP4 layer on CTA pairs, token tiles of BN rows, after the routing.
+template <int BN>
 moe_status launch_mx_pair(const moe_layer *L, const void *x, int T, void *out, void *ws,
                           const WsLayout &W, cudaStream_t st) {
   const moe_config &c = L->cfg;
   const size_t P = (size_t)T * (c.top_k + c.n_shared), G = (size_t)c.n_experts + c.n_shared;
-  const size_t tiles = P / kMxPairBN + G, wblocks = G * (c.d_ff / 128) * (c.d_model / 128);
+  constexpr int kBlocks = scale_block_bytes(BN) / kMxScaleBlock;  // of a tile
+  const size_t tiles = P / BN + G, wblocks = G * (c.d_ff / 128) * (c.d_model / 128);
   MxPairParams p;
   memset(&p, 0, sizeof p);
   p.b = stream_base(L, x, T, out, ws, W);
@@ -1579,14 +1590,22 @@ moe_status launch_mx_pair(const moe_layer *L, const void *x, int T, void *out, v
             encode_scale_blocks(&p.tm_su, L->sc_up, wblocks, 1) &&
             encode_scale_blocks(&p.tm_sd, L->sc_down, wblocks, 1) &&
             encode_scale_blocks(&p.tm_xs, at<uint8_t>(ws, W.x_scale),
-                                tiles * 2 * (c.d_model / 128), 2) &&
-            encode_scale_blocks(&p.tm_hs, p.hs, tiles * 2 * (c.d_ff / 128), 2);
+                                tiles * kBlocks * (c.d_model / 128), kBlocks) &&
+            encode_scale_blocks(&p.tm_hs, p.hs, tiles * kBlocks * (c.d_ff / 128), kBlocks);
   for (int i = 0; i < 3; ++i)
-    ok = ok && encode_u8_2d(&p.tm_x[i], xs, c.d_model, 2 * P, pair_box(i)) &&
-         encode_u8_2d(&p.tm_h[i], p.h.hi, c.d_ff, 2 * P, pair_box(i));
+    ok = ok && encode_u8_2d(&p.tm_x[i], xs, c.d_model, 2 * P, pair_box<BN>(i)) &&
+         encode_u8_2d(&p.tm_h[i], p.h.hi, c.d_ff, 2 * P, pair_box<BN>(i));
   if (!ok) return MOE_ERR_CUDA;
-  return launch_cl(mxfp4_pair_kernel, dim3(L->mx_pair_grid), dim3(kMxPairThreads), MxPairCfg::SMEM,
-                   st, 2, p);
+  moe_status s = launch(split_rows_kernel<BN>,
+                        dim3(grid_for((size_t)T * ((c.d_model + 511) / 512), 8, L->num_sms)),
+                        dim3(256), 0, st, static_cast<const __nv_bfloat16 *>(x),
+                        (const int *)at<int>(ws, W.slot_row), (const int *)at<int>(ws, W.idx),
+                        (const int *)at<int>(ws, W.offsets), T, c.d_model, c.n_experts, c.top_k,
+                        c.n_shared, split_rows(at<uint8_t>(ws, W.x_split), P, c.d_model),
+                        at<uint8_t>(ws, W.x_scale));
+  if (s != MOE_OK) return s;
+  return launch_cl(mxfp4_pair_kernel<BN>, dim3(L->mx_pair_grid[BN == 112]), dim3(kMxPairThreads),
+                   MxPairCfg<BN>::SMEM, st, 2, p);
 }
 
 template <int NT>
@@ -1626,23 +1645,17 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
   const CounterReset reset{status->sched, at<int>(ws, W.done),
                            c.n_experts + c.n_shared + 1 + c.d_model / kStreamMinTile};
   float *logits = at<float>(ws, W.logits);
-  const size_t P = (size_t)T * (c.top_k + c.n_shared);
   moe_status s;
   if ((s = launch_logits(L, x, T, logits, at<float>(ws, W.part), status, st)) != MOE_OK ||
       (s = launch_select_permute(L, logits, T, nullptr, at<int>(ws, W.idx),
                                  at<float>(ws, W.gate), at<int>(ws, W.counts),
                                  at<int>(ws, W.offsets), at<int>(ws, W.perm),
                                  at<int>(ws, W.slot_row), at<int>(ws, W.chunk_hist), reset,
-                                 st)) != MOE_OK ||
-      (s = launch(split_rows_kernel,
-                  dim3(grid_for((size_t)T * ((c.d_model + 511) / 512), 8, L->num_sms)), dim3(256), 0,
-                  st, static_cast<const __nv_bfloat16 *>(x), at<int>(ws, W.slot_row),
-                  at<int>(ws, W.idx), at<int>(ws, W.offsets), T, c.d_model, c.n_experts, c.top_k,
-                  c.n_shared, kMxPairBN,
-                  split_rows(at<uint8_t>(ws, W.x_split), P, c.d_model),
-                  at<uint8_t>(ws, W.x_scale))) != MOE_OK)
+                                 st)) != MOE_OK)
     return s;
-  if ((s = launch_mx_pair(L, x, T, out, ws, W, st)) != MOE_OK) return s;
+  s = mx_token_tile(c, T) == 32 ? launch_mx_pair<32>(L, x, T, out, ws, W, st)
+                                : launch_mx_pair<112>(L, x, T, out, ws, W, st);
+  if (s != MOE_OK) return s;
   return launch(mxfp4_combine_kernel,
                 dim3(grid_for((size_t)T * (c.d_model / 4), 256, L->num_sms)), dim3(256), 0, st,
                 (const float *)at<float>(ws, W.y), (const int *)at<int>(ws, W.slot_row),

@@ -18,12 +18,10 @@
 // Scales are copied to TMEM by tcgen05.cp in the order of the instruction's scale layout: blocks of
 // 512 bytes for 128 rows x 128 K, byte (r % 32) * 16 + r / 32 * 4 + k / 32.
 //
-// Bound at 16 tokens by the weight stream: 884 MB in 183 us, 0.74 of the copy rate (a stage of 17 KB
-// of codes fills 33 KB of shared memory, so a ring of 5 or 6 stages holds 90 KB in flight; asking
-// tiles into L2 ahead of their load made it 14 % slower).  At 1 token by latency: 10 us of routing,
-// then 90 up units of 32 stages on 148 SMs, the down units, the combine.  One token tile of 8, 16 or
-// 32 rows covers every token of the calls that it is chosen for, so no weight is read twice below
-// 33 tokens; wider tiles would only shorten the ring.
+// Bound at 16 tokens by the weight stream: 884 MB in 176 us, 0.77 of the copy rate (a stage of 17 KB
+// of codes fills 33 KB of shared memory, so a ring of 5 or 6 stages holds 90 to 100 KB in flight;
+// asking tiles into L2 ahead of their load made it 14 % slower).  At 1 token by latency: 10 us of
+// routing, then 90 up units of 32 stages on 148 SMs, the down units, the combine.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -53,13 +51,10 @@ __host__ __forceinline__ SplitRows split_rows(uint8_t *values, size_t rows, int 
 // Their scales come in blocks as the weights' do, one (or two, one behind the other, past 128 rows)
 // for each token tile and 128 columns (token_tile_number): of a tile with n tokens, rows 0 .. n - 1
 // are hi's; lo's begin at row BN, or on CTA pairs, whose N follows n, at the next multiple of 8.
-constexpr int kMxPairBN = 112;  // token rows of a CTA pair's tile (mxfp4_pair.cuh)
 __host__ __device__ constexpr int scale_block_bytes(int BN) {
   return (2 * BN + 127) / 128 * kMxScaleBlock;
 }
-__device__ __forceinline__ int scale_lo_row(int n, int BN) {
-  return BN == kMxPairBN ? (n + 7) & ~7 : BN;
-}
+__device__ __forceinline__ int pair_lo_row(int n) { return (n + 7) & ~7; }
 __device__ __forceinline__ int scale_row_at(int r) {
   return (r >> 7) * kMxScaleBlock + (r & 31) * 16 + ((r >> 5) & 3) * 4;
 }
@@ -250,13 +245,14 @@ __device__ __forceinline__ void store_h_chunk(const SplitRows &h, uint8_t *hs, i
   }
 }
 
-// x [T, d] -> the split rows of the sorted space with their scale blocks: token t to its k routed
-// rows and its shared row.  One warp converts 512 columns of a token and stores them k + n_shared
-// times; bound by HBM (2 d bytes read, 2 d (k + n_shared) written a token).
+// x [T, d] -> the split rows of the sorted space with the scale blocks of CTA pairs' tiles of BN rows:
+// token t to its k routed rows and its shared row.  One warp converts 512 columns of a token and
+// stores them k + n_shared times; bound by HBM (2 d bytes read, 2 d (k + n_shared) written a token).
+template <int BN>
 __global__ void __launch_bounds__(256)
     split_rows_kernel(const __nv_bfloat16 *__restrict__ x, const int *__restrict__ slot_row,
                       const int *__restrict__ idx, const int *__restrict__ offsets, int T, int d,
-                      int E, int k, int n_shared, int BN, SplitRows out, uint8_t *xs) {
+                      int E, int k, int n_shared, SplitRows out, uint8_t *xs) {
   const int lane = threadIdx.x & 31, nk = d / 128, n_warps = gridDim.x * 8;
   const int chunks = (d + 511) / 512;
   griddep_wait();
@@ -273,7 +269,7 @@ __global__ void __launch_bounds__(256)
     auto place = [&](int g, int off, int rows, int row, int &tile, int &r, int &r_lo) {
       tile = token_tile_number(off, g, (row - off) / BN, BN);
       r = (row - off) % BN;
-      r_lo = scale_lo_row(min(BN, rows - (row - off - r)), BN) + r;
+      r_lo = pair_lo_row(min(BN, rows - (row - off - r))) + r;
     };
     int row = 0, tile = 0, r = 0, r_lo = 0, s_tile, s_r, s_lo;
     if (lane < k) {

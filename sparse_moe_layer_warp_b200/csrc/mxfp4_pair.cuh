@@ -1,16 +1,18 @@
 // mxfp4_pair.cuh -- the experts over MXFP4 weights on CTA pairs (tcgen05 cta_group::2), for groups of
 // many tokens.  Arithmetic, units and waits are mxfp4_layer.cuh's.
 //
-// What bounds mxfp4_layer_kernel there is shared memory: a stage of two 128-row weight tiles and
-// 56 tokens takes 448 clocks of tensor time, but its operands cross the 128 bytes a clock of shared
+// What would bound one-CTA tiles there is shared memory: a stage of two 128-row weight tiles and 56
+// tokens takes 448 clocks of tensor time, but its operands cross the 128 bytes a clock of shared
 // memory for 830 (codes are one byte there; they are written by the copy, and read once for every
 // 112 columns of N).  A pair runs M = 256, N = 224: a CTA's codes are read once for 112 tokens, and
 // each CTA holds and reads only half of the token rows -- the hi rows in the leader, the lo rows in
-// its peer.  A stage of 896 clocks then moves 106 KB: the tensor cores bind again.
+// its peer.  A stage of 896 clocks then moves 106 KB, and the tensor cores bind (8192 tokens: 1.95
+// ms, the tensor pipe 71 % active, 1.35 GHz under the power cap).  256 tokens stream 2.4 GB of weights
+// in 0.42 ms, 0.88 of the copy rate.
 //
 // CTA r of a pair holds weight rows [128 r, 128 r + 128) of each 256-row tile; a unit has two tiles
 // (gate and up; two neighbours of W_d).  N follows the unit's tokens (2 x the next multiple of 8).
-// TMEM: 2 x 224 accumulator columns, so one unit at a time, and two sets of scales.  The scales of
+// TMEM: 2 x 224 accumulator columns (of 112-token tiles), so one unit at a time, and two sets of scales.  The scales of
 // all N columns are needed by both CTAs, those of the weight rows by the CTA that holds them.
 // The combine is a launch of its own: at these sizes y is larger than L2 and wants every warp.
 #pragma once
@@ -31,24 +33,31 @@ struct MxPairParams {
   CUtensorMap tm_g, tm_u, tm_d;      // codes, box {128, 128}, padded 4-bit
   CUtensorMap tm_sg, tm_su, tm_sd;   // their scale blocks as words, box {128, 1}
   CUtensorMap tm_x[3], tm_h[3];      // token rows, hi then lo [2 P, cols]: boxes of pair_box rows
-  CUtensorMap tm_xs, tm_hs;          // scale blocks as words, box {128, 2}
+  CUtensorMap tm_xs, tm_hs;          // scale blocks as words, box {128, blocks of a tile}
   SplitRows h;
   uint8_t *hs;
 };
 
 // Rows of the three token boxes: a tile of few tokens loads few rows.
-__host__ __device__ constexpr int pair_box(int i) { return i == 0 ? 16 : (i == 1 ? 56 : kMxPairBN); }
+template <int BN>
+__host__ __device__ constexpr int pair_box(int i) {
+  return i == 2 ? BN : (i == 1 ? BN / 2 : (BN > 32 ? 16 : 8));
+}
 
+// BN: token rows of a tile.  112 where the tensor cores bind.  16 where weights are streamed for a few
+// rows of each expert: what counts is then the ring, six stages against four.
+template <int kBN>
 struct MxPairCfg {
-  static constexpr int BN = kMxPairBN;
+  static constexpr int BN = kBN;
   static constexpr int A_BYTES = 2 * kMxTile * 128;
   static constexpr int B_BYTES = BN * 128;  // hi rows (leader) or lo rows (peer)
   static constexpr int SA_BYTES = 2 * kMxScaleBlock, SB_BYTES = scale_block_bytes(BN);
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
   static constexpr int TILE_COLS = 2 * BN, ACC_COLS = 2 * TILE_COLS;
   static constexpr int SF_COLS = 24;  // for each of the two MMA warps: weights 4, tokens 8
-  static constexpr int TMEM_COLS = 512;
-  static_assert(ACC_COLS + 2 * SF_COLS <= TMEM_COLS && SB_BYTES == 1024, "TMEM");
+  static constexpr int TMEM_USED = ACC_COLS + 2 * SF_COLS;
+  static constexpr int TMEM_COLS = TMEM_USED <= 128 ? 128 : 512;
+  static_assert(TMEM_USED <= TMEM_COLS && BN % 16 == 0 && 2 * BN <= 256, "tile");
   static constexpr int FIXED = StreamTables::BYTES + 1024 /*barriers*/ + 1024 /*alignment*/;
   static constexpr int STAGES = (226 * 1024 - FIXED) / STAGE_BYTES;
   static_assert(STAGES >= 4 && B_BYTES % 1024 == 0, "pipeline");
@@ -72,10 +81,11 @@ __device__ __forceinline__ void tc_cp_scales_pair(uint32_t taddr, uint32_t smem_
                : "memory");
 }
 
+template <int BN>
 __global__ void __launch_bounds__(kMxPairThreads, 1)
     mxfp4_pair_kernel(const __grid_constant__ MxPairParams p) {
-  using C = MxPairCfg;
-  constexpr int S = C::STAGES, BN = C::BN;
+  using C = MxPairCfg<BN>;
+  constexpr int S = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -251,7 +261,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         __syncwarp();  // the elected lane's copies follow those two loads
         fence_proxy_async_global();  // other CTAs' stores, read by TMA
       }
-      const int nk = (up ? d : f) / 128, box = w.n <= pair_box(0) ? 0 : (w.n <= pair_box(1) ? 1 : 2);
+      const int nk = (up ? d : f) / 128, box = w.n <= pair_box<BN>(0) ? 0 : (w.n <= pair_box<BN>(1) ? 1 : 2);
       const CUtensorMap *m = up ? &p.tm_x[box] : &p.tm_h[box], *sc = up ? &p.tm_xs : &p.tm_hs;
       for (int kc = 0; kc < nk; ++kc) {
         ok = warp_wait(&empty[st], ph ^ 1, 35);
@@ -259,10 +269,11 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
         if (elect_one()) {
           const uint32_t bar = full_leader + st * 8;
           if (leader)
-            mbar_arrive_expect_tx(&full[st], 2 * (pair_box(box) * 128 + C::SB_BYTES));
+            mbar_arrive_expect_tx(&full[st], 2 * (pair_box<BN>(box) * 128 + C::SB_BYTES));
           tma_load_2d_pair(sB + st * C::B_BYTES, m, bar, kc * 128, (int)rank * n_rows + w.row0,
                            pol);
-          tma_load_2d_pair(sSB + st * C::SB_BYTES, sc, bar, 0, (w.tile * nk + kc) * 2, pol);
+          tma_load_2d_pair(sSB + st * C::SB_BYTES, sc, bar, 0,
+                           (w.tile * nk + kc) * (C::SB_BYTES / kMxScaleBlock), pol);
         }
         __syncwarp();
         ++filled;
@@ -286,7 +297,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
       const uint32_t a_base = smem_u32(sA) + j * (C::A_BYTES / 2), b_base = smem_u32(sB),
                      sa_base = smem_u32(sSA) + j * kMxScaleBlock, sb_base = smem_u32(sSB);
       while (next_unit(w, 36) && w.kind >= 0) {
-        const int nk = (w.kind == 0 ? d : f) / 128, half = scale_lo_row(w.n, BN);
+        const int nk = (w.kind == 0 ? d : f) / 128, half = pair_lo_row(w.n);
         const bool there = tile_row(w, j, 0) < (w.kind == 0 ? f : d);
         const uint32_t id0 = idesc_mx(256, 2 * half);
         bool ok = warp_wait(tempty, (it & 1) ^ 1, 46), ready = false;
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
               const uint32_t sb = sb_base + st * C::SB_BYTES;
               tc_cp_scales_pair(sf, sa_base + st * C::SA_BYTES);
               tc_cp_scales_pair(sf + 4, sb);
-              if (half > 64) tc_cp_scales_pair(sf + 8, sb + kMxScaleBlock);
+              if (BN > 64 && half > 64) tc_cp_scales_pair(sf + 8, sb + kMxScaleBlock);
               const uint64_t a = sdesc_k_sw128(a_base + st * C::A_BYTES),
                              b = sdesc_k_sw128(b_base + st * C::B_BYTES);
 #pragma unroll
@@ -341,7 +352,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
     Unit w;
     while ((alive = next_unit(w, 42)) && w.kind >= 0) {
       const bool up = w.kind == 0;
-      const int m_rows = up ? f : d, half = scale_lo_row(w.n, BN);
+      const int m_rows = up ? f : d, half = pair_lo_row(w.n);
       const int row_a = tile_row(w, 0, rank), row_b = tile_row(w, 1, rank);
       const bool one = row_a < m_rows, two = row_b < m_rows;
       alive = warp_wait(tfull, it & 1, 39);

@@ -184,8 +184,9 @@ struct StreamTables {
     slot = perm + kStreamMaxPairs;
     gate = reinterpret_cast<float *>(slot + kStreamMaxPairs);
   }
-  // largest size: 1025 groups without, or 289 groups with the routing of 512 pairs
-  static constexpr int BYTES = 12 * 1024;
+  // largest size: 1025 groups without, or 289 groups with the routing of 512 pairs (no more: at
+  // 9 KB the smallest stages would not fit six times)
+  static constexpr int BYTES = 17 * 512;
 };
 static_assert((2 * (kMaxExperts + 1) + 1) * 4 <= StreamTables::BYTES, "tables");
 static_assert((2 * (kDecodeMaxExperts + 1) + 1 + 3 * kStreamMaxPairs) * 4 <= StreamTables::BYTES,

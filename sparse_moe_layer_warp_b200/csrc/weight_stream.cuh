@@ -12,6 +12,9 @@
 // A stage holds 32 weight rows x 256 columns; lane t of a row's four lanes takes 16-byte chunk 2t or
 // 2t + 1 of each 64 columns, which the swizzle spreads over all banks (the order of K inside a
 // block of 32 is free as long as both operands agree on it).
+//
+// Bound by HBM: 16 tokens stream 3.3 GB in 0.50 to 0.55 ms (0.92 to 1.0 of the copy rate), 1 token
+// 285 MB in 63 us, of which routing is 10 and the combine 3.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -1569,6 +1569,12 @@ bool encode_scale_blocks(CUtensorMap *m, const void *base, uint64_t n, uint32_t 
          CUDA_SUCCESS;
 }
 
+// Blocks for all the work at once: of short blocks the device always has the next ones ready (8192
+// tokens: 2643 us with 16 blocks an SM that loop, 2596 without).
+dim3 grid_whole(size_t work, int per_block) {
+  return dim3((unsigned)((work + per_block - 1) / per_block));
+}
+
 // The experts of the MXFP4 layer on CTA pairs, token tiles of BN rows, after the routing.
 template <int BN>
 moe_status launch_mx_pair(const moe_layer *L, const void *x, int T, void *out, void *ws,
@@ -1597,7 +1603,7 @@ moe_status launch_mx_pair(const moe_layer *L, const void *x, int T, void *out, v
          encode_u8_2d(&p.tm_h[i], p.h.hi, c.d_ff, 2 * P, pair_box<BN>(i));
   if (!ok) return MOE_ERR_CUDA;
   moe_status s = launch(split_rows_kernel<BN>,
-                        dim3(grid_for((size_t)T * ((c.d_model + 511) / 512), 8, L->num_sms)),
+                        grid_whole((size_t)T * ((c.d_model + 511) / 512), 8),
                         dim3(256), 0, st, static_cast<const __nv_bfloat16 *>(x),
                         (const int *)at<int>(ws, W.slot_row), (const int *)at<int>(ws, W.idx),
                         (const int *)at<int>(ws, W.offsets), T, c.d_model, c.n_experts, c.top_k,
@@ -1657,7 +1663,7 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
                                 : launch_mx_pair<112>(L, x, T, out, ws, W, st);
   if (s != MOE_OK) return s;
   return launch(mxfp4_combine_kernel,
-                dim3(grid_for((size_t)T * (c.d_model / 4), 256, L->num_sms)), dim3(256), 0, st,
+                grid_whole((size_t)T * (c.d_model / 4), 256), dim3(256), 0, st,
                 (const float *)at<float>(ws, W.y), (const int *)at<int>(ws, W.slot_row),
                 (const float *)at<float>(ws, W.gate), c.routed_scale, T, c.top_k, c.n_shared,
                 c.d_model, static_cast<__nv_bfloat16 *>(out));

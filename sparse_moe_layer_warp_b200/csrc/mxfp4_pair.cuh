@@ -6,9 +6,9 @@
 // memory for 830 (codes are one byte there; they are written by the copy, and read once for every
 // 112 columns of N).  A pair runs M = 256, N = 224: a CTA's codes are read once for 112 tokens, and
 // each CTA holds and reads only half of the token rows -- the hi rows in the leader, the lo rows in
-// its peer.  A stage of 896 clocks then moves 106 KB, and the tensor cores bind (8192 tokens: 1.95
+// its peer.  A stage of 896 clocks then moves 106 KB, and the tensor cores bind (8192 tokens: 1.84
 // ms, the tensor pipe 71 % active, 1.35 GHz under the power cap).  256 tokens stream 2.4 GB of weights
-// in 0.42 ms, 0.88 of the copy rate.
+// in 0.39 ms, 0.94 of the copy rate.
 //
 // CTA r of a pair holds weight rows [128 r, 128 r + 128) of each 256-row tile; a unit has two tiles
 // (gate and up; two neighbours of W_d).  N follows the unit's tokens (2 x the next multiple of 8).

@@ -329,7 +329,15 @@ __device__ __forceinline__ void schedule_units(const StreamBase &p, const Stream
         down = true;
       }
       const int tiles = down ? down_tiles : up_tiles;
-      while (tb.tile_prefix[pos + 1] * tiles <= u) ++pos;
+      // bisection: with few tokens most groups are empty, and stepping over 288 of them took 8 us
+      if (tb.tile_prefix[pos + 1] * tiles <= u) {
+        int last = G - 1;
+        while (pos < last) {
+          const int mid = (pos + last) >> 1;
+          if (tb.tile_prefix[mid + 1] * tiles <= u) pos = mid + 1;
+          else last = mid;
+        }
+      }
       r.g = group_at(p, pos);
       r.uses = tb.tile_prefix[pos + 1] - tb.tile_prefix[pos];
       const int loc = u - tb.tile_prefix[pos] * tiles;

@@ -401,7 +401,9 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     // the grid barrier gave up: no unit is claimed
   } else if (warp == 9) {
     if (lane == 0)
-      schedule_units(p.b, tb, BN, up_tiles, down_tiles, blockIdx.x, gridDim.x,
+      schedule_units(p.b, tb, BN, up_tiles, down_tiles,
+                     tickets_by_position(blockIdx.x, gridDim.x),
+                     [&] { return atomicAdd(p.b.sched, 1); },
                      [&](const Unit &r) {
                        if (!mbar_wait_suspend(&uq_empty[qi], qph ^ 1, abort_flag, p.b.status, 31))
                          return false;

@@ -133,6 +133,11 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   if (warp == kMxPairEpiWarps) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
   griddep_wait();
   griddep_launch_dependents();
+  // The scheduler's first ticket, asked for here: its round trip passes behind the tables.  Pairs of
+  // one grid need not run at once (another kernel may hold SMs), so none has units by position.
+  auto claim = [&] { return atomicAdd(p.b.sched, 1); };
+  int first_ticket = 0;
+  if (warp == kMxPairEpiWarps && !leader && lane == 0) first_ticket = claim();
   for (int e = threadIdx.x; e <= p.b.E; e += blockDim.x) tb.offsets[e] = p.b.offsets[e];
   __syncthreads();
   if (warp == 0) build_tile_prefix(p.b, tb, BN);
@@ -174,7 +179,8 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   if (warp == kMxPairEpiWarps && !leader) {
     // ---------------------------------------------------------------- scheduler (peer)
     if (lane == 0)
-      schedule_units(p.b, tb, BN, up_tiles, down_tiles, blockIdx.x >> 1, gridDim.x >> 1,
+      schedule_units(p.b, tb, BN, up_tiles, down_tiles,
+                     tickets_claimed(first_ticket, claim), claim,
                      [&](const Unit &r) {
                        if (!mbar_wait_suspend<true>(&uq_empty[qi], qph ^ 1, abort_flag, p.b.status,
                                                     31))

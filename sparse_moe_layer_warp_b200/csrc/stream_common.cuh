@@ -15,10 +15,12 @@
 // down units.
 //
 // Waiting: a down unit's token rows wait for counts of finished h rows, the combine for counts of
-// finished y rows.  A unit is only ever claimed by a CTA (or pair) that runs, and finishing it waits
-// for up units alone (claimed before), so these waits end whatever the residency of the grid.  The
-// one-launch layer adds one barrier of the grid after the router's logits, so it is a cooperative
-// launch.  All waits are bounded.
+// finished y rows.  Finishing a unit waits for up units alone, whose tickets are lower, and a CTA
+// takes its own in order: these waits end if whoever owns an up unit runs.  The CTA pairs draw every
+// ticket from the counter, so only a pair that runs owns any, whatever the residency of the grid.
+// The one-launch layer has a barrier of the grid after the router's logits and is a cooperative launch
+// for that: all its CTAs run at once, and each owns its first tickets by position.  All waits are
+// bounded.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -49,7 +51,7 @@ struct StreamBase {
   float *logits;                           // [T, E]
   int *done, *done_all, *tile_done;        // finished pieces of h of a group, of all groups; of y
                                            // of a d tile (zero at launch, or zeroed by the kernel)
-  int *sched;                              // units claimed beyond each CTA's first kClaimAhead
+  int *sched;                              // tickets drawn from the counter (Tickets)
   int *grid_bar;                           // one-launch layer: arrivals, departures
   DevStatus *status;
   int T, d, f, E, k, n_shared;
@@ -177,7 +179,7 @@ struct StreamTables {
   int *offsets;      // [E + 1]
   int *perm, *slot;  // one-launch layer: [Tk]
   float *gate;
-  __device__ __forceinline__ StreamTables(void *mem, int E, int n_shared) {
+  __host__ __device__ __forceinline__ StreamTables(void *mem, int E, int n_shared) {
     tile_prefix = static_cast<int *>(mem);
     offsets = tile_prefix + (E + n_shared + 1);
     perm = offsets + (E + 1);
@@ -272,10 +274,10 @@ __device__ __forceinline__ bool route_tokens(const StreamBase &p, const StreamTa
   return true;
 }
 
-__device__ __forceinline__ int group_at(const StreamBase &p, int o) {
+__host__ __device__ __forceinline__ int group_at(const StreamBase &p, int o) {
   return p.n_shared ? (o == 0 ? p.E : o - 1) : o;
 }
-__device__ __forceinline__ int group_rows(const StreamBase &p, const StreamTables &tb, int g) {
+__host__ __device__ __forceinline__ int group_rows(const StreamBase &p, const StreamTables &tb, int g) {
   return g < p.E ? tb.offsets[g + 1] - tb.offsets[g] : p.T;
 }
 
@@ -300,29 +302,56 @@ __device__ __forceinline__ void build_tile_prefix(const StreamBase &p, const Str
   if (lane == 31) tb.tile_prefix[G] = incl;
 }
 
+// The kClaimAhead tickets that a scheduler has in hand, as the counter gave them (nothing is computed
+// from a claim before its turn: the thread would wait for the answer): ticket t is unit t + base.
+struct Tickets {
+  int t0, t1, t2, base;
+};
+static_assert(kClaimAhead == 3, "t0, t1, t2");
+// All drawn from the counter, t0 by the caller before: a scheduler that does not run yet owns no unit.
+// t2 is drawn once t1 has come, and t1 some time after t0, so that those who start together get units a
+// round apart: with three draws in a row a third of the pairs took all the units of a small batch
+// (200 tokens, 16 experts: 75 us, so drawn 60; 77 tokens of a small model 50, so drawn 46).
+template <typename Claim>
+__host__ __device__ __forceinline__ Tickets tickets_claimed(int t0, Claim claim) {
+  Tickets k;
+  k.t0 = t0;
+  k.t1 = claim();
+  k.t2 = k.t1 >= 0 ? claim() : 0;  // (no ticket is negative: this waits for t1)
+  k.base = 0;
+  return k;
+}
+// The first of scheduler `me` of n by position, which saves a round trip at the start.  Only where
+// all n schedulers are sure to run at once: another's first units are not done by anyone else.
+__host__ __device__ __forceinline__ Tickets tickets_by_position(int me, int n) {
+  Tickets k;
+  k.base = kClaimAhead * n;
+  k.t0 = me - k.base;
+  k.t1 = k.t0 + n;
+  k.t2 = k.t1 + n;
+  return k;
+}
+
 // The scheduler: one thread claims units until none is left and hands each, the end (kind -1) last,
-// to publish(unit), which returns false when a wait gave up.  Scheduler `me` of n.
-template <typename Publish>
-__device__ __forceinline__ void schedule_units(const StreamBase &p, const StreamTables &tb, int bt,
-                                               int up_tiles, int down_tiles, int me, int n,
-                                               Publish publish) {
+// to publish(unit), which returns false when a wait gave up.  claim() draws the counter's next ticket.
+template <typename Claim, typename Publish>
+__host__ __device__ __forceinline__ void schedule_units(const StreamBase &p,
+                                                        const StreamTables &tb, int bt,
+                                                        int up_tiles, int down_tiles, Tickets k,
+                                                        Claim claim, Publish publish) {
   const int G = p.E + p.n_shared, n_tiles = tb.tile_prefix[G];
   const int n_up = n_tiles * up_tiles, n_units = n_up + n_tiles * down_tiles;
   int pos = 0;  // group (in group order) of the last unit
   bool down = false;
-  // tickets in hand, as the counter gave them (nothing is computed from a claim before its
-  // turn: the thread would wait for the answer)
-  int t0 = me - kClaimAhead * n, t1 = t0 + n, t2 = t1 + n;
-  static_assert(kClaimAhead == 3, "t0, t1, t2");
   while (true) {
-    int u = t0 + kClaimAhead * n;
-    t0 = t1;
-    t1 = t2;
-    t2 = atomicAdd(p.sched, 1);
+    int u = k.t0 + k.base;
+    k.t0 = k.t1;
+    k.t1 = k.t2;
+    k.t2 = claim();
     Unit r;
     r.kind = u < n_up ? 0 : (u < n_units ? 1 : -1);
     if (r.kind >= 0) {
-      // a CTA's tickets only grow, so the group is found from the last one's on
+      // a scheduler's tickets only grow, so the group is found from the last one's on
       if (r.kind == 1) {
         u -= n_up;
         if (!down) pos = 0;

@@ -150,13 +150,17 @@ def _check(fn: str, status: int) -> None:
         raise MoEError(fn, status)
 
 
+def _dense(t) -> None:
+    if not t.is_contiguous():
+        raise ValueError(f"the library takes contiguous (dense row-major) tensors; got shape "
+                         f"{tuple(t.shape)} with strides {tuple(t.stride())}")
+
+
 def _addr(t) -> int:
     """Device address of a tensor handed to the C ABI.  The library reads and writes dense
     row-major device memory through raw pointers, so a strided view or a host tensor is
     refused here, before anything is launched."""
-    if not t.is_contiguous():
-        raise ValueError(f"the library takes contiguous (dense row-major) tensors; got shape "
-                         f"{tuple(t.shape)} with strides {tuple(t.stride())}")
+    _dense(t)
     if not t.is_cuda:
         raise ValueError(f"the library takes CUDA tensors; got one on {t.device}")
     return t.data_ptr()
@@ -473,13 +477,15 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
     lead, cols = tuple(codes.shape[:-1]), 2 * int(codes.shape[-1])
     _expect(codes, lead + (cols // 2,), torch.uint8, "codes")
     _expect(scales, lead + (cols // MXFP4_BLOCK,), torch.uint8, "scales")
-    _addr(codes)
+    _dense(codes)
+    _dense(scales)
+    p_codes, p_scales = _addr(codes), _addr(scales)
     if scales.device != codes.device:
         raise ValueError(f"scales: on {scales.device}, codes on {codes.device}")
     out = codes.new_empty(lead + (cols,), dtype=dtype)
     if n := out.numel():
-        _call_on_device_of(codes, "moe_mxfp4_dequantize", codes.data_ptr(), scales.data_ptr(),
-                           n // cols, cols, out.data_ptr(), _DTYPE_CODE[dtype], stream=stream)
+        _call_on_device_of(codes, "moe_mxfp4_dequantize", p_codes, p_scales, n // cols,
+                           cols, out.data_ptr(), _DTYPE_CODE[dtype], stream=stream)
     return out
 
 

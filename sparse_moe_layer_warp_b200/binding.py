@@ -175,20 +175,71 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _call_on_device_of(t, fn, *args, stream=None) -> None:
-    """Library call `fn` with a last argument of the stream, with t's device current.  The device is
-    switched and the stream looked up only where needed: for a small matrix these take longer than
-    the kernel."""
-    dev = t.get_device()
-    call = getattr(load_library(), fn)
-    if dev == torch.cuda.current_device():
-        raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-        status = call(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            raw = (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-            status = call(*args, raw)
-    _check(fn, status)
+class _Here:
+    """The caller's device and stream are the call's: nothing to switch or to hand over."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+    @staticmethod
+    def new(t):
+        return t
+
+
+_HERE = _Here()
+
+
+class _There:
+    """A call's device and stream made current: what it allocates comes from the pool of the stream
+    that writes it.  Memory that crosses between that stream and the caller's goes back to its pool
+    only once the other is done with it: the caller's `tensors`, and results (`new`)."""
+
+    def __init__(self, dev, stream, tensors):
+        self.caller = None
+        if stream is None:
+            self.ctx = torch.cuda.device(dev)
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=dev)
+        if stream.device.index != dev:
+            raise ValueError(f"stream: of {stream.device}, the call's tensors are on cuda:{dev}")
+        self.ctx = torch.cuda.stream(stream)
+        self.caller = torch.cuda.current_stream(dev)
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
+
+    def __enter__(self):
+        self.ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc)
+
+    def new(self, t):
+        if self.caller is not None:
+            t.record_stream(self.caller)
+        return t
+
+
+def _on(dev, stream, *tensors):
+    """Context of a call on `stream` (None: the current one) of device `dev` that reads or writes the
+    caller's `tensors`.  Switches only where needed: for a small matrix that takes longer than the
+    kernel."""
+    if dev == torch._C._cuda_getDevice() and (
+            stream is None
+            or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(dev)):
+        return _HERE
+    return _There(dev, stream, tensors)
+
+
+def _call_here(dev, fn, *args) -> None:
+    """Library call `fn` on the current stream of device `dev`, its last argument."""
+    _check(fn, getattr(_lib or load_library(), fn)(
+        *args, torch._C._cuda_getCurrentRawStream(dev)))
 
 
 # ------------------------------------------------------------------ C-ABI mirrors
@@ -451,19 +502,22 @@ def moe_gemm_clock(handle, ws, stream=None) -> tuple:
 # ------------------------------------------------------------------ MXFP4 matrices
 def mxfp4_quantize(w, stream=None):
     """(codes [.., cols / 2], scales [.., cols / 32]), uint8, of `w` [.., cols] (fp32 or bf16,
-    contiguous, cols a multiple of 32): MXFP4, one power-of-two scale for 32 neighbours."""
-    if w.dtype not in _DTYPE_CODE:
+    contiguous, cols a multiple of 32): MXFP4, one power-of-two scale for 32 neighbours.  On `stream`
+    (default: the current one), which the caller orders after whatever wrote w."""
+    dtype = _DTYPE_CODE.get(w.dtype)
+    if dtype is None:
         raise ValueError(f"w: expected fp32 or bf16, got {w.dtype}")
-    if w.dim() < 1 or w.shape[-1] % MXFP4_BLOCK:
+    *lead, cols = w.shape or (1,)
+    if cols % MXFP4_BLOCK:
         raise ValueError(f"w: the last dimension must be a multiple of {MXFP4_BLOCK}, got shape "
                          f"{tuple(w.shape)}")
-    _addr(w)
-    lead, cols = w.shape[:-1], w.shape[-1]
-    codes = w.new_empty((*lead, cols // 2), dtype=torch.uint8)
-    scales = w.new_empty((*lead, cols // MXFP4_BLOCK), dtype=torch.uint8)
-    if n := w.numel():
-        _call_on_device_of(w, "moe_mxfp4_quantize", w.data_ptr(), _DTYPE_CODE[w.dtype], n // cols,
-                           cols, codes.data_ptr(), scales.data_ptr(), stream=stream)
+    p, dev = _addr(w), w.get_device()
+    with _on(dev, stream, w) as on:
+        codes = on.new(w.new_empty((*lead, cols // 2), dtype=torch.uint8))
+        scales = on.new(w.new_empty((*lead, cols // MXFP4_BLOCK), dtype=torch.uint8))
+        if n := w.numel():
+            _call_here(dev, "moe_mxfp4_quantize", p, dtype, n // cols, cols, codes.data_ptr(),
+                       scales.data_ptr())
     return codes, scales
 
 
@@ -471,21 +525,23 @@ def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
     """The values [.., cols] that codes [.., cols / 2] and scales [.., cols / 32] stand for."""
     if dtype not in _DTYPE_CODE:
         raise ValueError(f"dtype: expected fp32 or bf16, got {dtype}")
-    if codes.dim() < 1 or (2 * codes.shape[-1]) % MXFP4_BLOCK:
+    *lead, half = codes.shape or (1,)
+    if half % (MXFP4_BLOCK // 2):
         raise ValueError(f"codes: the last dimension must be a multiple of {MXFP4_BLOCK // 2}, "
                          f"got shape {tuple(codes.shape)}")
-    lead, cols = tuple(codes.shape[:-1]), 2 * int(codes.shape[-1])
-    _expect(codes, lead + (cols // 2,), torch.uint8, "codes")
-    _expect(scales, lead + (cols // MXFP4_BLOCK,), torch.uint8, "scales")
-    _dense(codes)
+    cols = 2 * half
+    if codes.dtype != torch.uint8:
+        raise ValueError(f"codes: expected uint8, got {codes.dtype}")
+    _expect(scales, (*lead, cols // MXFP4_BLOCK), torch.uint8, "scales")
     _dense(scales)
-    p_codes, p_scales = _addr(codes), _addr(scales)
-    if scales.device != codes.device:
+    p_codes, p_scales, dev = _addr(codes), _addr(scales), codes.get_device()
+    if scales.get_device() != dev:
         raise ValueError(f"scales: on {scales.device}, codes on {codes.device}")
-    out = codes.new_empty(lead + (cols,), dtype=dtype)
-    if n := out.numel():
-        _call_on_device_of(codes, "moe_mxfp4_dequantize", p_codes, p_scales, n // cols,
-                           cols, out.data_ptr(), _DTYPE_CODE[dtype], stream=stream)
+    with _on(dev, stream, codes, scales) as on:
+        out = on.new(codes.new_empty((*lead, cols), dtype=dtype))
+        if n := out.numel():
+            _call_here(dev, "moe_mxfp4_dequantize", p_codes, p_scales, n // cols, cols,
+                       out.data_ptr(), _DTYPE_CODE[dtype])
     return out
 
 

@@ -555,7 +555,11 @@ def _expect(t, shape, dtype, name):
 
 
 class MoELayer:
-    """Owns a handle and a workspace; holds references to the weight tensors."""
+    """Owns a handle and a workspace; holds references to the weight tensors.
+
+    Calls run on `stream` (None: the current one), which the caller orders after whatever wrote
+    their inputs; results, and a workspace that a call has to allocate, come from that stream's
+    pool.  Calls of a layer share its workspace: on several streams the caller orders them."""
 
     def __init__(self, w_router, router_bias, w_gate, w_up, w_down, top_k: int,
                  max_tokens: int, n_shared: int = 1, routed_scale: float = 1.0):
@@ -574,12 +578,20 @@ class MoELayer:
                               int(n_shared), dt, float(routed_scale))
         self.tensors = (w_router, router_bias, w_gate, w_up, w_down)
         self.handle = moe_layer_init(self.cfg, *self.tensors)
+        self._start(w_router)
+
+    def _start(self, w_router):
         self.device = w_router.device
         self.dtype = w_router.dtype
         self.ws = None
         self.ws_need = {}  # bytes by number of tokens
         self.bw_ws = None
-        self.E, self.k, self.d = int(E), int(top_k), int(d)
+        self._ws_streams = {"ws": set(), "bw_ws": set()}  # (raw) streams that use each
+        self.E, self.k, self.d = (int(self.cfg.n_experts), int(self.cfg.top_k),
+                                  int(self.cfg.d_model))
+
+    def _on(self, stream, *tensors):
+        return _on(self.device.index, stream, *tensors)
 
     def _rows(self, x, name="x"):
         """Token count of a [T, d] activation of the layer's type."""
@@ -591,38 +603,67 @@ class MoELayer:
     def router_logits_static(self, x, logits_out=None, stream=None):
         """Router logits [T, E] fp32 through the workspace-free entry point."""
         T = self._rows(x)
-        if logits_out is None:
-            logits_out = torch.empty((T, self.E), dtype=torch.float32, device=self.device)
-        _expect(logits_out, (T, self.E), torch.float32, "logits_out")
-        moe_router_logits_static(self.handle, x, T, logits_out, stream, d_model=self.d,
-                                 n_experts=self.E, dtype=self.dtype)
+        with self._on(stream, x, logits_out) as on:
+            if logits_out is None:
+                logits_out = on.new(torch.empty((T, self.E), dtype=torch.float32,
+                                                device=self.device))
+            _expect(logits_out, (T, self.E), torch.float32, "logits_out")
+            moe_router_logits_static(self.handle, x, T, logits_out, d_model=self.d,
+                                     n_experts=self.E, dtype=self.dtype)
         return logits_out
 
     def set_option(self, option: int, value: int) -> None:
         moe_set_option(self.handle, option, value)
 
     def workspace(self, n_tokens: int, stream=None):
+        """The workspace, large enough for calls of up to n_tokens tokens and ready for a call on any
+        stream."""
+        with self._on(stream):
+            before = self.ws
+            ws = self._workspace(n_tokens)
+            if ws is not before and not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+        return ws
+
+    def _workspace(self, n_tokens: int):
         need = self.ws_need.get(n_tokens)
         if need is None:
             need = self.ws_need[n_tokens] = moe_workspace_size(self.handle, n_tokens)
-        if self.ws is None or self.ws.numel() < need:
-            self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            moe_workspace_init(self.handle, self.ws, stream)  # before the first call that uses it
-        return self.ws
+        return self._reserve("ws", need)
+
+    def _reserve(self, name, need):
+        """self.ws or self.bw_ws for a call on the current stream, replaced if it is smaller than need
+        bytes."""
+        ws, users = getattr(self, name), self._ws_streams[name]
+        raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+        if ws is None or ws.numel() < need:
+            # The old one goes back to the pool of the stream that allocated it, once every stream
+            # that used it is done (record_stream below).
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            setattr(self, name, ws)
+            users.clear()
+            users.add(raw)
+            moe_workspace_init(self.handle, ws)  # before the first call that uses it
+        elif raw not in users:
+            ws.record_stream(torch.cuda.current_stream())
+            users.add(raw)
+        return ws
 
     def forward(self, x, out=None, stream=None):
         T = self._rows(x)
-        out = torch.empty_like(x) if out is None else out
-        _expect(out, x.shape, x.dtype, "out")
-        moe_forward(self.handle, x, T, out, self.workspace(T, stream), stream)
+        with self._on(stream, x, out) as on:
+            out = on.new(torch.empty_like(x)) if out is None else out
+            _expect(out, x.shape, x.dtype, "out")
+            moe_forward(self.handle, x, T, out, self._workspace(T))
         return out
 
     def forward_few(self, x, out=None, stream=None):
         """forward for a few tokens in one launch (bf16; limits in include/moe_layer.h)."""
         T = self._rows(x)
-        out = torch.empty_like(x) if out is None else out
-        _expect(out, x.shape, x.dtype, "out")
-        moe_forward_few(self.handle, x, T, out, self.workspace(T, stream), stream)
+        with self._on(stream, x, out) as on:
+            out = on.new(torch.empty_like(x)) if out is None else out
+            _expect(out, x.shape, x.dtype, "out")
+            moe_forward_few(self.handle, x, T, out, self._workspace(T))
         return out
 
     def to_mxfp4(self, max_tokens: int | None = None) -> "MoELayerMXFP4":
@@ -642,24 +683,23 @@ class MoELayer:
         else:
             T = int(logits.shape[0])
             _expect(logits, (T, self.E), torch.float32, "logits")
-        dev = self.device
-        r = dict(
-            idx=torch.empty((T, self.k), dtype=torch.int32, device=dev),
-            gates=torch.empty((T, self.k), dtype=torch.float32, device=dev),
-            counts=torch.empty((self.E,), dtype=torch.int32, device=dev),
-            offsets=torch.empty((self.E + 1,), dtype=torch.int32, device=dev),
-            perm=torch.empty((T * self.k,), dtype=torch.int32, device=dev),
-            slot_row=torch.empty((T, self.k), dtype=torch.int32, device=dev))
-        ws = self.workspace(T)
-        if logits is not None:
-            moe_route_from_logits(self.handle, logits, T, r["idx"], r["gates"], r["counts"],
-                                  r["offsets"], r["perm"], r["slot_row"], ws, stream)
-        else:
-            lg = torch.empty((T, self.E), dtype=torch.float32, device=dev) if want_logits else None
-            moe_route(self.handle, x, T, lg, r["idx"], r["gates"], r["counts"], r["offsets"],
-                      r["perm"], r["slot_row"], ws, stream)
-            if lg is not None:
-                r["logits"] = lg
+        with self._on(stream, x, logits) as on:
+            def new(*shape, dtype=torch.int32):
+                return on.new(torch.empty(shape, dtype=dtype, device=self.device))
+
+            r = dict(idx=new(T, self.k), gates=new(T, self.k, dtype=torch.float32),
+                     counts=new(self.E), offsets=new(self.E + 1), perm=new(T * self.k),
+                     slot_row=new(T, self.k))
+            ws = self._workspace(T)
+            if logits is not None:
+                moe_route_from_logits(self.handle, logits, T, r["idx"], r["gates"], r["counts"],
+                                      r["offsets"], r["perm"], r["slot_row"], ws)
+            else:
+                lg = new(T, self.E, dtype=torch.float32) if want_logits else None
+                moe_route(self.handle, x, T, lg, r["idx"], r["gates"], r["counts"], r["offsets"],
+                          r["perm"], r["slot_row"], ws)
+                if lg is not None:
+                    r["logits"] = lg
         return r
 
     def router_stats(self, logits, topk_idx, n_groups, stream=None):
@@ -667,25 +707,27 @@ class MoELayer:
         T = int(logits.shape[0])
         _expect(logits, (T, self.E), torch.float32, "logits")
         _expect(topk_idx, (T, self.k), torch.int32, "topk_idx")
-        p_mean = torch.empty(self.E, dtype=torch.float32, device=self.device)
-        f_sel = torch.empty(self.E, dtype=torch.float32, device=self.device)
-        scalars = torch.empty(2, dtype=torch.float32, device=self.device)
-        moe_router_stats(self.handle, logits, topk_idx, T, n_groups, p_mean, f_sel, scalars,
-                         self.workspace(T), stream)
+        with self._on(stream, logits, topk_idx) as on:
+            p_mean, f_sel, scalars = (
+                on.new(torch.empty(n, dtype=torch.float32, device=self.device))
+                for n in (self.E, self.E, 2))
+            moe_router_stats(self.handle, logits, topk_idx, T, n_groups, p_mean, f_sel, scalars,
+                             self._workspace(T))
         return p_mean, f_sel, scalars
 
     def forward_save(self, x, out=None, saved=None, stream=None):
         """Training forward (bf16): (out, saved) with `saved` the fp32 pre-activations that
         backward(..., saved=saved) reads instead of recomputing them."""
         T = self._rows(x)
-        ws = self.workspace(T)
-        if out is None:
-            out = torch.empty_like(x)
-        _expect(out, x.shape, x.dtype, "out")
-        if saved is None:
-            saved = torch.empty(moe_saved_size(self.handle, T) // 4, dtype=torch.float32,
-                                device=self.device)
-        moe_forward_save(self.handle, x, T, out, saved, ws, stream)
+        with self._on(stream, x, out, saved) as on:
+            ws = self._workspace(T)
+            if out is None:
+                out = on.new(torch.empty_like(x))
+            _expect(out, x.shape, x.dtype, "out")
+            if saved is None:
+                saved = on.new(torch.empty(moe_saved_size(self.handle, T) // 4,
+                                           dtype=torch.float32, device=self.device))
+            moe_forward_save(self.handle, x, T, out, saved, ws)
         return out, saved
 
     def backward(self, x, dout, stream=None, grads=None, saved=None, overwrite=False):
@@ -695,10 +737,15 @@ class MoELayer:
         pre-activations are not recomputed."""
         T = self._rows(x)
         _expect(dout, x.shape, x.dtype, "dout")
-        need = moe_backward_workspace_size(self.handle, T)
-        if self.bw_ws is None or self.bw_ws.numel() < need:
-            self.bw_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            moe_workspace_init(self.handle, self.bw_ws)
+        with self._on(stream, x, dout, saved, *(grads or {}).values()) as on:
+            g = self._backward(x, T, dout, grads, saved, overwrite)
+            for name in g:
+                if grads is None or name == "dx":
+                    on.new(g[name])
+        return g
+
+    def _backward(self, x, T, dout, grads, saved, overwrite):
+        bw_ws = self._reserve("bw_ws", moe_backward_workspace_size(self.handle, T))
         G = self.E + int(self.cfg.n_shared)
         f = int(self.cfg.d_ff)
         kw = dict(dtype=torch.float32, device=self.device)
@@ -722,38 +769,38 @@ class MoELayer:
             _expect(g[name], shape, torch.float32, name)
         if overwrite:
             moe_backward_ex(self.handle, x, T, dout, saved, MOE_BACKWARD_OVERWRITE, g["dx"],
-                            g["dw_router"], g["dw_gate"], g["dw_up"], g["dw_down"], self.bw_ws,
-                            stream)
+                            g["dw_router"], g["dw_gate"], g["dw_up"], g["dw_down"], bw_ws)
         elif saved is not None:
             moe_backward_saved(self.handle, x, T, dout, saved, g["dx"], g["dw_router"],
-                               g["dw_gate"], g["dw_up"], g["dw_down"], self.bw_ws, stream)
+                               g["dw_gate"], g["dw_up"], g["dw_down"], bw_ws)
         else:
             moe_backward(self.handle, x, T, dout, g["dx"], g["dw_router"], g["dw_gate"],
-                         g["dw_up"], g["dw_down"], self.bw_ws, stream)
+                         g["dw_up"], g["dw_down"], bw_ws)
         return g
 
     def expert_health(self, n_tokens, stream=None):
         """act_rms [G], param_norm [G], ratios [2] of the last forward of n_tokens tokens."""
         G = self.E + int(self.cfg.n_shared)
-        act = torch.empty(G, dtype=torch.float32, device=self.device)
-        par = torch.empty(G, dtype=torch.float32, device=self.device)
-        ratios = torch.empty(2, dtype=torch.float32, device=self.device)
-        moe_expert_health(self.handle, n_tokens, act, par, ratios, self.workspace(n_tokens),
-                          stream)
+        with self._on(stream) as on:
+            act, par, ratios = (on.new(torch.empty(n, dtype=torch.float32, device=self.device))
+                                for n in (G, G, 2))
+            moe_expert_health(self.handle, n_tokens, act, par, ratios, self._workspace(n_tokens))
         return act, par, ratios
 
     def gemm_clock_mhz(self, stream=None) -> tuple:
         """(up, down) effective SM clock of the forward's expert GEMMs since the last call, for
         forwards run with MOE_OPTION_GEMM_CLOCK set (see moe_gemm_clock)."""
-        return moe_gemm_clock(self.handle, self.ws, stream)
+        with self._on(stream):
+            return moe_gemm_clock(self.handle, self.ws)
 
     def device_status(self, stream=None) -> int:
         """Device status of the forward's and the backward's workspaces (0: no bounded wait
         gave up in either)."""
         st = 0
-        for ws in (self.ws, self.bw_ws):
-            if ws is not None:
-                st = st or moe_device_status(self.handle, ws, stream)
+        with self._on(stream):
+            for ws in (self.ws, self.bw_ws):
+                if ws is not None:
+                    st = st or moe_device_status(self.handle, ws)
         return st
 
     def close(self):
@@ -802,12 +849,7 @@ class MoELayerMXFP4(MoELayer):
             torch.cuda.current_stream().synchronize()  # calls may come on any stream
         self.tensors = (w_router, router_bias, *tiled)
         self.handle = moe_layer_init_mxfp4(self.cfg, *self.tensors)
-        self.device = w_router.device
-        self.dtype = w_router.dtype
-        self.ws = None
-        self.ws_need = {}  # bytes by number of tokens
-        self.bw_ws = None
-        self.E, self.k, self.d = int(E), int(top_k), int(d)
+        self._start(w_router)
 
     def to_mxfp4(self, max_tokens: int | None = None):
         raise ValueError("to_mxfp4: the layer holds MXFP4 weights already")

@@ -1,0 +1,127 @@
+"""Layer calls on a stream other than the caller's own: whose memory results and workspaces are, and
+when it is given back.  A stream is held back by a sleeping kernel, so that the order of what follows on
+it is known."""
+import pytest
+import torch
+
+from tests.test_mxfp4_gpu import Case
+from tests.test_mxfp4_streams_gpu import _hold, other  # noqa: F401  (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+KW = dict(d=512, E=16, k=4, f=256)
+
+
+def _calls(layer):
+    """name: call(x, stream) -> list of results, for a layer of either kind."""
+    return dict(
+        forward=lambda x, s: [layer.forward(x, stream=s)],
+        forward_few=lambda x, s: [layer.forward_few(x[:16], stream=s)],
+        route=lambda x, s: list(layer.route(x=x, want_logits=True, stream=s).values()),
+        router_logits_static=lambda x, s: [layer.router_logits_static(x[:16], stream=s)])
+
+
+NAMES = ["forward", "forward_few", "route", "router_logits_static"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("mx", [False, True])
+def test_results_on_another_stream(other, name, mx):  # noqa: F811
+    """No result takes a block that the caller's stream still uses; none dropped early, or read by the
+    caller and dropped, is given to anyone else too soon."""
+    c = Case(T=100, **KW)
+    layer = c.layer(mx)
+    call = _calls(layer)[name]
+    want = [t.clone() for t in call(c.x, None)]
+    torch.cuda.synchronize()
+    # in use on the caller's stream
+    blocks = [torch.empty_like(t) for t in want for _ in range(2)]
+    torch.cuda.synchronize()
+    _hold()
+    for b in blocks:
+        b.fill_(1)
+    del b, blocks
+    got = call(c.x, other)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # dropped before it is written
+    del got
+    _hold(other)
+    call(c.x, other)
+    fresh = [torch.empty_like(t).fill_(3) for t in want for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all((t == 3).all() for t in fresh)
+    # read by the caller, who has waited for it, and dropped while the read is held back
+    got = call(c.x, other)
+    torch.cuda.current_stream().wait_stream(other)
+    _hold()
+    read = [t.clone() for t in got]
+    del got
+    x2 = Case(T=100, seed=1, **KW).x
+    again = call(x2, other)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(read, want))
+    assert not all(torch.equal(a, b) for a, b in zip(again, want))
+    assert layer.device_status() == 0
+
+
+@pytest.mark.parametrize("T1,T2", [(4, 60), (60, 300), (200, 300)])
+@pytest.mark.parametrize("mx", [False, True])
+def test_workspace_replaced_while_in_use(other, mx, T1, T2):  # noqa: F811
+    """A larger call replaces the workspace that a call on another stream still uses: its memory is not
+    handed out before that call is done."""
+    c = Case(T=T2, **KW)
+    x1 = c.x[:T1].contiguous()
+    want1 = c.layer(mx).forward(x1).clone()
+    want2 = c.layer(mx).forward(c.x).clone()
+    layer = c.layer(mx)
+    size = layer.workspace(T1).numel()
+    torch.cuda.synchronize()
+    out1 = torch.empty_like(x1)
+    _hold(other)
+    layer.forward(x1, out=out1, stream=other)
+    out2 = layer.forward(c.x)
+    assert layer.ws.numel() > size
+    fresh = [torch.empty(size, dtype=torch.uint8, device="cuda").fill_(255) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(out1, want1) and torch.equal(out2, want2)
+    assert all((t == 255).all() for t in fresh)
+    assert layer.device_status() == 0
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_workspace_reserved_for_another_stream(other, mx):  # noqa: F811
+    """workspace(T) on the caller's stream, which is held back, then the first call on another."""
+    c = Case(T=70, **KW)
+    want = c.layer(mx).forward(c.x).clone()
+    layer = c.layer(mx)
+    torch.cuda.synchronize()
+    _hold()
+    layer.workspace(70)
+    out = torch.empty_like(c.x)
+    layer.forward(c.x, out=out, stream=other)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and layer.device_status() == 0
+
+
+def test_training_calls_on_another_stream(other):  # noqa: F811
+    """The first forward_save and backward of a layer, on a stream beside a held-back caller's."""
+    c = Case(T=40, **KW)
+    layer, dout = c.layer(False), c.x.flip(0).contiguous()
+    out, saved = layer.forward_save(c.x)
+    want = [out, *layer.backward(c.x, dout, saved=saved).values()]
+    stats = layer.router_stats(*(layer.route(x=c.x, want_logits=True)[n] for n in ("logits", "idx")),
+                               n_groups=4)
+    health = layer.expert_health(40)
+    torch.cuda.synchronize()
+    layer = c.layer(False)
+    _hold()
+    out, saved = layer.forward_save(c.x, stream=other)
+    got = [out, *layer.backward(c.x, dout, saved=saved, stream=other).values()]
+    h = layer.expert_health(40, stream=other)
+    r = layer.route(x=c.x, want_logits=True, stream=other)
+    s = layer.router_stats(r["logits"], r["idx"], n_groups=4, stream=other)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(torch.equal(a, b) for a, b in zip((*h, *s), (*health, *stats)))
+    assert layer.device_status() == 0

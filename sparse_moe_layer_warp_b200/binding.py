@@ -559,7 +559,9 @@ class MoELayer:
 
     Calls run on `stream` (None: the current one), which the caller orders after whatever wrote
     their inputs; results, and a workspace that a call has to allocate, come from that stream's
-    pool.  Calls of a layer share its workspace: on several streams the caller orders them."""
+    pool.  Calls of a layer share its workspace: on several streams the caller orders them.  A
+    workspace that a captured call uses lives as long as the layer, so its graph may be replayed
+    after calls of any size; the graph needs the layer to live."""
 
     def __init__(self, w_router, router_bias, w_gate, w_up, w_down, top_k: int,
                  max_tokens: int, n_shared: int = 1, routed_scale: float = 1.0):
@@ -587,6 +589,9 @@ class MoELayer:
         self.ws_need = {}  # bytes by number of tokens
         self.bw_ws = None
         self._ws_streams = {"ws": set(), "bw_ws": set()}  # (raw) streams that use each
+        self._ws_clear = {"ws": False, "bw_ws": False}  # cleared by a call that was not captured
+        self._ws_captured = {"ws": False, "bw_ws": False}  # used by a captured call
+        self._kept = []  # replaced workspaces that graphs use
         self.E, self.k, self.d = (int(self.cfg.n_experts), int(self.cfg.top_k),
                                   int(self.cfg.d_model))
 
@@ -636,17 +641,26 @@ class MoELayer:
         bytes."""
         ws, users = getattr(self, name), self._ws_streams[name]
         raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+        capturing = torch.cuda.is_current_stream_capturing()
         if ws is None or ws.numel() < need:
             # The old one goes back to the pool of the stream that allocated it, once every stream
-            # that used it is done (record_stream below).
+            # that used it is done (record_stream below), or never, if a graph has its address.
+            if self._ws_captured[name]:
+                self._kept.append(ws)
             ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             setattr(self, name, ws)
             users.clear()
             users.add(raw)
-            moe_workspace_init(self.handle, ws)  # before the first call that uses it
+            self._ws_clear[name] = self._ws_captured[name] = False
         elif raw not in users:
             ws.record_stream(torch.cuda.current_stream())
             users.add(raw)
+        if not self._ws_clear[name]:
+            # before the first call that uses it; a captured clearing only runs with its graph
+            moe_workspace_init(self.handle, ws)
+            self._ws_clear[name] = not capturing
+        if capturing:
+            self._ws_captured[name] = True
         return ws
 
     def forward(self, x, out=None, stream=None):

@@ -125,3 +125,88 @@ def test_training_calls_on_another_stream(other):  # noqa: F811
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert all(torch.equal(a, b) for a, b in zip((*h, *s), (*health, *stats)))
     assert layer.device_status() == 0
+
+
+def _capture(call):
+    """The call in a graph, after one of the same on a side stream."""
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    return g
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T", [16, 100])
+def test_graph_replayed_after_a_larger_call(cuda_ok, mx, T):
+    """The workspace of a captured call outlives its replacement by a larger call's."""
+    c = Case(T=300, **KW)
+    x = c.x[:T].contiguous()
+    layer, out = c.layer(mx), torch.empty_like(x)
+    want, want_big = c.layer(mx).forward(x).clone(), c.layer(mx).forward(c.x).clone()
+    g = _capture(lambda: layer.forward(x, out=out))
+    size = layer.ws.numel()
+    assert torch.equal(layer.forward(c.x), want_big)
+    assert layer.ws.numel() > size
+    fresh = [torch.empty(size, dtype=torch.uint8, device="cuda").fill_(255) for _ in range(4)]
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert torch.equal(layer.forward(c.x), want_big)
+    assert all((t == 255).all() for t in fresh)
+    assert layer.device_status() == 0
+
+
+def test_backward_graph_replayed_after_a_larger_call(cuda_ok):
+    c = Case(T=100, **KW)
+    x, dout = c.x[:8].contiguous(), c.x[8:16].contiguous()
+    layer = c.layer(False)
+    grads = {n: t for n, t in layer.backward(x, dout).items() if n != "dx"}
+    want = {n: t.clone() for n, t in grads.items()}
+    res = {}
+
+    def step():
+        res["g"] = layer.backward(x, dout, grads=grads, overwrite=True)
+
+    g = _capture(step)
+    size = layer.bw_ws.numel()
+    layer.backward(c.x, c.x)
+    assert layer.bw_ws.numel() > size
+    fresh = [torch.empty(size, dtype=torch.uint8, device="cuda").fill_(255) for _ in range(4)]
+    for t in grads.values():
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(grads[n], want[n]) for n in want)
+    assert all((t == 255).all() for t in fresh)
+    assert layer.device_status() == 0
+
+
+@pytest.mark.parametrize("mx", [False, True])
+@pytest.mark.parametrize("T", [16, 100])
+def test_first_call_of_a_layer_captured(cuda_ok, mx, T):
+    """A workspace allocated by a captured call is cleared in every replay, and by the first call outside
+    the graph; whatever its memory held before."""
+    c = Case(T=T, **KW)
+    want = c.layer(mx).forward(c.x).clone()
+    layer, out = c.layer(mx), torch.empty_like(c.x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer.forward(c.x, out=out)
+    layer.ws.fill_(0xAB)
+    assert torch.equal(layer.forward(c.x), want)
+    layer.ws.fill_(0xAB)
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert torch.equal(layer.forward(c.x), want)
+    assert layer.device_status() == 0

@@ -200,7 +200,8 @@ moe_status moe_set_option(moe_handle h, int option, int value);
 
 /* Bytes of device workspace a call with n_tokens tokens needs (0 on bad arguments).
  * The workspace holds the routing scratch, the expert-sorted activations, the SwiGLU
- * outputs h and the per-row expert outputs y between the kernels of one call. */
+ * outputs h and the per-row expert outputs y between the kernels of one call.  Does not fall as
+ * n_tokens grows: a workspace for n_tokens serves every smaller call. */
 size_t moe_workspace_size(moe_handle h, int n_tokens);
 
 /* Clears the workspace's device status word (call once after allocating a workspace). */

@@ -20,10 +20,12 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stdint.h>
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 #include <utility>
 
@@ -248,7 +250,8 @@ int n_splits(const moe_config &c) { return (c.d_model + kSplitKSlice - 1) / kSpl
 
 size_t esize(const moe_config &c) { return c.dtype == MOE_BF16 ? 2 : 4; }
 
-// Workspace regions (256-byte aligned).  P = T*k + n_shared*T rows of the sorted space.
+// Workspace regions (256-byte aligned).  P = T*k + n_shared*T rows of the sorted space.  The total
+// does not fall as T grows: a workspace for T tokens serves every smaller call.
 struct WsLayout {
   size_t status, logits, part, idx, gate, counts, offsets, perm, slot_row, chunk_hist, stats,
       xs, h, y, done, health, x_split, x_scale, h_scale, total;
@@ -265,9 +268,12 @@ bool up_gathers_rows(const moe_config &c, int T) {
 
 // The one-launch layer: at most 64 tokens and 512 (token, slot) pairs, and the decode router's
 // limits (every CTA selects for all tokens).
-bool few_shape(const moe_config &c, int T) {
-  return decode_route_ok(c, T) && T <= kStreamMaxT && T * c.top_k <= kStreamMaxPairs;
+int few_limit(const moe_config &c) {
+  static_assert(kStreamMaxT <= kChunk, "the decode router's tokens");
+  const int by_pairs = kStreamMaxPairs / c.top_k;
+  return !decode_route_ok(c, 1) ? 0 : by_pairs < kStreamMaxT ? by_pairs : kStreamMaxT;
 }
+bool few_shape(const moe_config &c, int T) { return T <= few_limit(c); }
 
 // Token rows of a tile of the MXFP4 layer, by the mean rows of an expert: a smaller tile leaves room
 // for more stages of weights in flight, a larger one reads weights again less often.  At 288 experts,
@@ -275,10 +281,27 @@ bool few_shape(const moe_config &c, int T) {
 // 512, 578 / 600 at 768; with skewed routing 246 / 240 at 256, 348 / 313 at 512.  One launch with 8 /
 // 16 / 32: 175 / 182 / 186 at 16 tokens, 383 / 396 / 399 at 64; 32 experts and 64 tokens 180 / 176 /
 // 184; 8 experts and 32 tokens 107 / 101 / 98.
+struct MxTile {
+  bool few;      // one launch
+  int rows;      // of a token tile
+  int last;      // largest number of tokens (of the one launch, then of CTA pairs)
+};
+constexpr int kMxTiles = 5;
+void mx_tiles(const moe_config &c, MxTile (&t)[kMxTiles]) {
+  const int few = few_limit(c), E = c.n_experts, k = c.top_k;
+  auto up_to = [&](int tokens) { return tokens < few ? tokens : few; };
+  t[0] = {true, 8, up_to(4 * E / k > 8 ? 4 * E / k : 8)};
+  t[1] = {true, 16, up_to(16 * E / k > 16 ? 16 * E / k : 16)};
+  t[2] = {true, 32, few};
+  t[3] = {false, 32, 12 * E / k};
+  t[4] = {false, 112, INT_MAX};
+}
 int mx_token_tile(const moe_config &c, int T) {
-  const long long pairs = (long long)T * c.top_k, E = c.n_experts;
-  if (!few_shape(c, T)) return pairs <= 12 * E ? 32 : 112;
-  return T <= 8 || pairs <= 4 * E ? 8 : T <= 16 || pairs <= 16 * E ? 16 : 32;
+  MxTile t[kMxTiles];
+  mx_tiles(c, t);
+  int i = 0;
+  while (T > t[i].last) ++i;
+  return t[i].rows;
 }
 
 // mx: an MXFP4 handle's layout (x and h as pairs of e4m3 values with their scales; x by token for
@@ -296,7 +319,7 @@ WsLayout ws_layout(const moe_config &c, int T, bool mx = false) {
   const size_t nch = ((size_t)T + kChunk - 1) / kChunk;
   L.status = take(sizeof(DevStatus));
   L.logits = take((size_t)T * c.n_experts * 4);
-  L.part = take((T <= kSplitKTokens ? (size_t)n_splits(c) : 0) * T * c.n_experts * 4);
+  L.part = take((size_t)n_splits(c) * (T < kSplitKTokens ? T : kSplitKTokens) * c.n_experts * 4);
   L.idx = take(Tk * 4);
   L.gate = take(Tk * 4);
   // counts, offsets and chunk histograms hold kMaxTopK more buckets than experts: the drop
@@ -314,13 +337,27 @@ WsLayout ws_layout(const moe_config &c, int T, bool mx = false) {
   L.done = take(((size_t)c.n_experts + c.n_shared + 1 + c.d_model / kStreamMinTile) * 4);
   // expert health: slice sums of squares, activations then parameters
   L.health = take(2 * ((size_t)c.n_experts + c.n_shared) * kHealthSlices * 8);
-  const size_t x_rows = !mx ? 0 : few_shape(c, T) ? (size_t)T : P;
+  // Split x, and scale blocks of every token tile (x of the one-launch layer: words by token), the
+  // most that T tokens or fewer need: smaller token tiles have more scale blocks.
+  size_t x_rows = 0, x_scale = 0, h_scale = 0;
+  if (mx) {
+    MxTile t[kMxTiles];
+    mx_tiles(c, t);
+    int before = 0;
+    for (const MxTile &m : t) {
+      const int n = T < m.last ? T : m.last;
+      if (n <= before) continue;  // no call of T tokens or fewer has this tile
+      before = n;
+      const size_t rows = (size_t)n * (c.top_k + c.n_shared);
+      const size_t blocks = (rows / m.rows + c.n_experts + c.n_shared) * scale_block_bytes(m.rows);
+      x_rows = std::max(x_rows, m.few ? (size_t)n : rows);
+      x_scale = std::max(x_scale, m.few ? (size_t)n * 8 : blocks);
+      h_scale = std::max(h_scale, blocks);
+    }
+  }
   L.x_split = take(2 * x_rows * c.d_model);
-  // scale blocks of every token tile (x of the one-launch layer: words by token)
-  const size_t block = scale_block_bytes(mx_token_tile(c, T));
-  const size_t tiles = !mx ? 0 : P / mx_token_tile(c, T) + c.n_experts + c.n_shared;
-  L.x_scale = take((few_shape(c, T) ? x_rows * 8 : tiles * block) * (c.d_model / 128));
-  L.h_scale = take(tiles * block * (c.d_ff / 128));
+  L.x_scale = take(x_scale * (c.d_model / 128));
+  L.h_scale = take(h_scale * (c.d_ff / 128));
   L.total = off;
   return L;
 }

@@ -1687,15 +1687,22 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
   DevStatus *status = at<DevStatus>(ws, W.status);
   const CounterReset reset{status->sched, at<int>(ws, W.done),
                            c.n_experts + c.n_shared + 1 + c.d_model / kStreamMinTile};
-  float *logits = at<float>(ws, W.logits);
+  float *logits = at<float>(ws, W.logits), *gate = at<float>(ws, W.gate);
+  int *idx = at<int>(ws, W.idx), *counts = at<int>(ws, W.counts);
+  int *offsets = at<int>(ws, W.offsets), *perm = at<int>(ws, W.perm);
+  int *slot_row = at<int>(ws, W.slot_row);
+  // the kernels of moe_route, so the selection is its
   moe_status s;
-  if ((s = launch_logits(L, x, T, logits, at<float>(ws, W.part), status, st)) != MOE_OK ||
-      (s = launch_select_permute(L, logits, T, nullptr, at<int>(ws, W.idx),
-                                 at<float>(ws, W.gate), at<int>(ws, W.counts),
-                                 at<int>(ws, W.offsets), at<int>(ws, W.perm),
-                                 at<int>(ws, W.slot_row), at<int>(ws, W.chunk_hist), reset,
-                                 st)) != MOE_OK)
-    return s;
+  if (decode_route_ok(c, T)) {
+    s = launch_route_decode(L, x, T, logits, idx, gate, counts, offsets, perm, slot_row, status,
+                            reset, st);
+  } else {
+    s = launch_logits(L, x, T, logits, at<float>(ws, W.part), status, st);
+    if (s == MOE_OK)
+      s = launch_select_permute(L, logits, T, nullptr, idx, gate, counts, offsets, perm, slot_row,
+                                at<int>(ws, W.chunk_hist), reset, st);
+  }
+  if (s != MOE_OK) return s;
   s = mx_token_tile(c, T) == 32 ? launch_mx_pair<32>(L, x, T, out, ws, W, st)
                                 : launch_mx_pair<112>(L, x, T, out, ws, W, st);
   if (s != MOE_OK) return s;
@@ -1709,7 +1716,8 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
 int mxfp4_launches(const moe_layer *L, int T) {
   if (T == 0) return 0;
   if (few_shape(L->cfg, T)) return 1;
-  return (T <= kChunk ? 2 : 3) + 3;  // routing; split rows, experts, combine
+  const int routing = decode_route_ok(L->cfg, T) ? 1 : T <= kChunk ? 2 : 3;
+  return routing + 3;  // split rows, experts, combine
 }
 }  // namespace
 

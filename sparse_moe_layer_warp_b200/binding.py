@@ -554,6 +554,14 @@ def _expect(t, shape, dtype, name):
                          f"{tuple(t.shape)} of {t.dtype}")
 
 
+def _expect_on(device, **tensors):
+    """A layer's kernels run on one device: an address of another one means nothing there."""
+    for name, t in tensors.items():
+        for part in t if isinstance(t, tuple) else (t,):
+            if part is not None and part.device != device:
+                raise ValueError(f"{name}: on {part.device}, the layer on {device}")
+
+
 class MoELayer:
     """Owns a handle and a workspace; holds references to the weight tensors.
 
@@ -576,10 +584,14 @@ class MoELayer:
         _expect(w_down, (G, d, f), w_router.dtype, "w_down")
         if router_bias is not None:
             _expect(router_bias, (E,), torch.float32, "router_bias")
+        _expect_on(w_router.device, router_bias=router_bias, w_gate=w_gate, w_up=w_up,
+                   w_down=w_down)
         self.cfg = moe_config(int(max_tokens), int(d), int(E), int(top_k), int(f),
                               int(n_shared), dt, float(routed_scale))
         self.tensors = (w_router, router_bias, w_gate, w_up, w_down)
-        self.handle = moe_layer_init(self.cfg, *self.tensors)
+        _addr(w_router)
+        with _on(w_router.get_device(), None):  # the handle is of this device
+            self.handle = moe_layer_init(self.cfg, *self.tensors)
         self._start(w_router)
 
     def _start(self, w_router):
@@ -598,21 +610,27 @@ class MoELayer:
     def _on(self, stream, *tensors):
         return _on(self.device.index, stream, *tensors)
 
+    def _expect(self, t, shape, dtype, name):
+        _expect(t, shape, dtype, name)
+        if t.get_device() != self.device.index:
+            raise ValueError(f"{name}: on {t.device}, the layer on {self.device}")
+
     def _rows(self, x, name="x"):
         """Token count of a [T, d] activation of the layer's type."""
         if x.dim() != 2:
             raise ValueError(f"{name}: expected a [T, {self.d}] tensor, got {tuple(x.shape)}")
-        _expect(x, (x.shape[0], self.d), self.dtype, name)
+        self._expect(x, (x.shape[0], self.d), self.dtype, name)
         return int(x.shape[0])
 
     def router_logits_static(self, x, logits_out=None, stream=None):
         """Router logits [T, E] fp32 through the workspace-free entry point."""
         T = self._rows(x)
+        if logits_out is not None:
+            self._expect(logits_out, (T, self.E), torch.float32, "logits_out")
         with self._on(stream, x, logits_out) as on:
             if logits_out is None:
                 logits_out = on.new(torch.empty((T, self.E), dtype=torch.float32,
                                                 device=self.device))
-            _expect(logits_out, (T, self.E), torch.float32, "logits_out")
             moe_router_logits_static(self.handle, x, T, logits_out, d_model=self.d,
                                      n_experts=self.E, dtype=self.dtype)
         return logits_out
@@ -665,18 +683,20 @@ class MoELayer:
 
     def forward(self, x, out=None, stream=None):
         T = self._rows(x)
+        if out is not None:
+            self._expect(out, x.shape, x.dtype, "out")
         with self._on(stream, x, out) as on:
             out = on.new(torch.empty_like(x)) if out is None else out
-            _expect(out, x.shape, x.dtype, "out")
             moe_forward(self.handle, x, T, out, self._workspace(T))
         return out
 
     def forward_few(self, x, out=None, stream=None):
         """forward for a few tokens in one launch (bf16; limits in include/moe_layer.h)."""
         T = self._rows(x)
+        if out is not None:
+            self._expect(out, x.shape, x.dtype, "out")
         with self._on(stream, x, out) as on:
             out = on.new(torch.empty_like(x)) if out is None else out
-            _expect(out, x.shape, x.dtype, "out")
             moe_forward_few(self.handle, x, T, out, self._workspace(T))
         return out
 
@@ -696,7 +716,7 @@ class MoELayer:
             T = self._rows(x)
         else:
             T = int(logits.shape[0])
-            _expect(logits, (T, self.E), torch.float32, "logits")
+            self._expect(logits, (T, self.E), torch.float32, "logits")
         with self._on(stream, x, logits) as on:
             def new(*shape, dtype=torch.int32):
                 return on.new(torch.empty(shape, dtype=dtype, device=self.device))
@@ -719,8 +739,8 @@ class MoELayer:
     def router_stats(self, logits, topk_idx, n_groups, stream=None):
         """p_mean [E], f_sel [E] and scalars [L_EP, routing confidence] (device tensors)."""
         T = int(logits.shape[0])
-        _expect(logits, (T, self.E), torch.float32, "logits")
-        _expect(topk_idx, (T, self.k), torch.int32, "topk_idx")
+        self._expect(logits, (T, self.E), torch.float32, "logits")
+        self._expect(topk_idx, (T, self.k), torch.int32, "topk_idx")
         with self._on(stream, logits, topk_idx) as on:
             p_mean, f_sel, scalars = (
                 on.new(torch.empty(n, dtype=torch.float32, device=self.device))
@@ -733,11 +753,12 @@ class MoELayer:
         """Training forward (bf16): (out, saved) with `saved` the fp32 pre-activations that
         backward(..., saved=saved) reads instead of recomputing them."""
         T = self._rows(x)
+        if out is not None:
+            self._expect(out, x.shape, x.dtype, "out")
         with self._on(stream, x, out, saved) as on:
             ws = self._workspace(T)
             if out is None:
                 out = on.new(torch.empty_like(x))
-            _expect(out, x.shape, x.dtype, "out")
             if saved is None:
                 saved = on.new(torch.empty(moe_saved_size(self.handle, T) // 4,
                                            dtype=torch.float32, device=self.device))
@@ -750,7 +771,7 @@ class MoELayer:
         or set when `overwrite`.  With `saved` (from forward_save of the same x) the
         pre-activations are not recomputed."""
         T = self._rows(x)
-        _expect(dout, x.shape, x.dtype, "dout")
+        self._expect(dout, x.shape, x.dtype, "dout")
         with self._on(stream, x, dout, saved, *(grads or {}).values()) as on:
             g = self._backward(x, T, dout, grads, saved, overwrite)
             for name in g:
@@ -780,7 +801,7 @@ class MoELayer:
                      dw_down=torch.zeros((G, self.d, f), **kw))
         for name, shape in (("dw_router", (self.E, self.d)), ("dw_gate", (G, f, self.d)),
                             ("dw_up", (G, f, self.d)), ("dw_down", (G, self.d, f))):
-            _expect(g[name], shape, torch.float32, name)
+            self._expect(g[name], shape, torch.float32, name)
         if overwrite:
             moe_backward_ex(self.handle, x, T, dout, saved, MOE_BACKWARD_OVERWRITE, g["dx"],
                             g["dw_router"], g["dw_gate"], g["dw_up"], g["dw_down"], bw_ws)
@@ -854,15 +875,18 @@ class MoELayerMXFP4(MoELayer):
         self.cfg = moe_config(int(max_tokens), int(d), int(E), int(top_k), int(f),
                               int(n_shared), MOE_BF16, float(routed_scale))
         self.handle = None
+        _expect_on(w_router.device, router_bias=router_bias, w_gate=tuple(w_gate),
+                   w_up=tuple(w_up), w_down=tuple(w_down))
         tiled = []
-        with torch.cuda.device(w_router.device):
+        _addr(w_router)
+        with _on(w_router.get_device(), None):
             for codes, scales in (w_gate, w_up, w_down):
                 t = torch.empty_like(scales)
                 moe_mxfp4_tile_scales(scales, t)
                 tiled.append((codes, t))
             torch.cuda.current_stream().synchronize()  # calls may come on any stream
-        self.tensors = (w_router, router_bias, *tiled)
-        self.handle = moe_layer_init_mxfp4(self.cfg, *self.tensors)
+            self.tensors = (w_router, router_bias, *tiled)
+            self.handle = moe_layer_init_mxfp4(self.cfg, *self.tensors)
         self._start(w_router)
 
     def to_mxfp4(self, max_tokens: int | None = None):

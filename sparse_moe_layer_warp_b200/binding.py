@@ -360,25 +360,41 @@ def moe_forward_few(handle, x, n_tokens, out, ws, stream=None) -> None:
 _DTYPE_CODE = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
+def _conversion(m, name, codes, scales):
+    """(rows, cols, dtype code) of matrix m, whose codes and scales have to go with it."""
+    if m.dtype not in _DTYPE_CODE:
+        raise ValueError(f"{name}: expected fp32 or bf16, got {m.dtype}")
+    n, cols = m.numel(), int(m.shape[-1])
+    for what, t, per in (("codes", codes, 2), ("scales", scales, MXFP4_BLOCK)):
+        _expect_bytes(what, t, n // per, m.device)
+    return n // max(cols, 1), cols, _DTYPE_CODE[m.dtype]
+
+
+def _expect_bytes(name, t, n, device):
+    if t.dtype != torch.uint8 or t.numel() != n or t.device != device:
+        raise ValueError(f"{name}: expected {n} bytes (uint8) on {device}, got {t.numel()} of "
+                         f"{t.dtype} on {t.device}")
+
+
 def moe_mxfp4_quantize(src, codes, scales, stream=None) -> None:
     """codes and scales of `src` [.., cols] (fp32 or bf16; see include/moe_layer.h)."""
-    cols = int(src.shape[-1])
+    rows, cols, dtype = _conversion(src, "src", codes, scales)
     _check("moe_mxfp4_quantize", load_library().moe_mxfp4_quantize(
-        _p(src), _DTYPE_CODE[src.dtype], src.numel() // max(cols, 1), cols, _p(codes),
-        _p(scales), _stream(stream)))
+        _p(src), dtype, rows, cols, _p(codes), _p(scales), _stream(stream)))
 
 
 def moe_mxfp4_dequantize(codes, scales, dst, stream=None) -> None:
     """The values that codes and scales stand for, into `dst` [.., cols] (fp32 or bf16)."""
-    cols = int(dst.shape[-1])
+    rows, cols, dtype = _conversion(dst, "dst", codes, scales)
     _check("moe_mxfp4_dequantize", load_library().moe_mxfp4_dequantize(
-        _p(codes), _p(scales), dst.numel() // max(cols, 1), cols, _p(dst),
-        _DTYPE_CODE[dst.dtype], _stream(stream)))
+        _p(codes), _p(scales), rows, cols, _p(dst), dtype, _stream(stream)))
 
 
 def moe_mxfp4_tile_scales(scales, tiled, stream=None) -> None:
     """`scales` [.., rows, cols / 32] in the order in which the layer's kernels load them."""
     kb = int(scales.shape[-1])
+    _expect_bytes("scales", scales, scales.numel(), scales.device)
+    _expect_bytes("tiled", tiled, scales.numel(), scales.device)
     _check("moe_mxfp4_tile_scales", load_library().moe_mxfp4_tile_scales(
         _p(scales), scales.numel() // max(kb, 1), kb * MXFP4_BLOCK, _p(tiled), _stream(stream)))
 

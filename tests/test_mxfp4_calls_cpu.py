@@ -151,3 +151,31 @@ def test_layer_calls_check_their_tensors_device(devices, monkeypatch):
         layer.forward_save(here)
     with pytest.raises(ValueError, match="on cuda:0"):
         layer.backward(there, here)
+
+
+def test_conversion_calls_check_sizes_and_types():
+    """The calls that take their results' tensors: one of another size would be written past its end."""
+    w = torch.zeros(4, 128, dtype=torch.bfloat16)
+    codes, scales = torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8)
+    q, d, t = (binding.moe_mxfp4_quantize, binding.moe_mxfp4_dequantize,
+               binding.moe_mxfp4_tile_scales)
+    with pytest.raises(ValueError, match="fp32 or bf16"):
+        q(w.half(), codes, scales)
+    with pytest.raises(ValueError, match="fp32 or bf16"):
+        d(codes, scales, w.half())
+    for c, s, name in ((codes[:3], scales, "codes"), (codes.int(), scales, "codes"),
+                       (codes, scales[:3], "scales"), (codes, scales.int(), "scales"),
+                       (codes.to("meta"), scales, "codes"), (codes, scales.to("meta"), "scales")):
+        with pytest.raises(ValueError, match=name):
+            q(w, c, s)
+        with pytest.raises(ValueError, match=name):
+            d(c, s, w)
+    for tiled in (scales[:3], scales.int(), scales.to("meta")):
+        with pytest.raises(ValueError, match="tiled"):
+            t(scales, tiled)
+    with pytest.raises(ValueError, match="scales"):
+        t(scales.int(), scales)
+    for call in (lambda: q(w, codes, scales), lambda: d(codes, scales, w),
+                 lambda: t(scales, scales.clone())):  # consistent: the pointers are looked at next
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            call()

@@ -84,6 +84,7 @@ struct moe_layer {
   const uint8_t *sc_gate, *sc_up, *sc_down;
   // the expert weights as the one-launch and MXFP4 kernels load them (bf16 or codes)
   CUtensorMap tm_st_g, tm_st_u, tm_st_d;
+  CUtensorMap tm_sc_g, tm_sc_u, tm_sc_d;  // MXFP4: their scale blocks, for the CTA pairs
 };
 
 namespace {
@@ -196,6 +197,20 @@ bool encode_bf16_3d(CUtensorMap *m, const void *base, uint64_t cols, uint64_t ro
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// 512-byte scale blocks [n] as words -> map with box {a block's 128 words, box_blocks}.
+bool encode_scale_blocks(CUtensorMap *m, const void *base, uint64_t n, uint32_t box_blocks) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {kMxScaleBlock / 4, n};
+  cuuint64_t strides[1] = {kMxScaleBlock};
+  cuuint32_t box[2] = {kMxScaleBlock / 4, box_blocks};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
@@ -897,7 +912,11 @@ static moe_status layer_init(const moe_config *cfg, const moe_weights *w, int e0
       L->sc_gate = mx->scale_gate;
       L->sc_up = mx->scale_up;
       L->sc_down = mx->scale_down;
-      if (!encode_codes(&L->tm_st_g, w->w_gate, c.d_model, G * c.d_ff) ||
+      const uint64_t blocks = G * (c.d_ff / 128) * (c.d_model / 128);
+      if (!encode_scale_blocks(&L->tm_sc_g, L->sc_gate, blocks, 1) ||
+          !encode_scale_blocks(&L->tm_sc_u, L->sc_up, blocks, 1) ||
+          !encode_scale_blocks(&L->tm_sc_d, L->sc_down, blocks, 1) ||
+          !encode_codes(&L->tm_st_g, w->w_gate, c.d_model, G * c.d_ff) ||
           !encode_codes(&L->tm_st_u, w->w_up, c.d_model, G * c.d_ff) ||
           !encode_codes(&L->tm_st_d, w->w_down, c.d_ff, G * c.d_model) ||
           !encode_bf16_2d(&L->tm_wr, w->w_router, c.d_model, c.n_experts, kBM) ||
@@ -1592,20 +1611,6 @@ moe_status launch_mx_few(const moe_layer *L, const void *x, int T, void *out, vo
   return launch_one(L, mxfp4_layer_kernel<BN>, p, kMxThreads, MxCfg<BN>::SMEM, st);
 }
 
-// 512-byte scale blocks [n] as words -> map with box {a block's 128 words, box_blocks}.
-bool encode_scale_blocks(CUtensorMap *m, const void *base, uint64_t n, uint32_t box_blocks) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {kMxScaleBlock / 4, n};
-  cuuint64_t strides[1] = {kMxScaleBlock};
-  cuuint32_t box[2] = {kMxScaleBlock / 4, box_blocks};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
-}
-
 // Blocks for all the work at once: of short blocks the device always has the next ones ready (8192
 // tokens: 2643 us with 16 blocks an SM that loop, 2596 without).
 dim3 grid_whole(size_t work, int per_block) {
@@ -1619,20 +1624,20 @@ moe_status launch_mx_pair(const moe_layer *L, const void *x, int T, void *out, v
   const moe_config &c = L->cfg;
   const size_t P = (size_t)T * (c.top_k + c.n_shared), G = (size_t)c.n_experts + c.n_shared;
   constexpr int kBlocks = scale_block_bytes(BN) / kMxScaleBlock;  // of a tile
-  const size_t tiles = P / BN + G, wblocks = G * (c.d_ff / 128) * (c.d_model / 128);
+  const size_t tiles = P / BN + G;
   MxPairParams p;
   memset(&p, 0, sizeof p);
   p.b = stream_base(L, x, T, out, ws, W);
   p.tm_g = L->tm_st_g;
   p.tm_u = L->tm_st_u;
   p.tm_d = L->tm_st_d;
+  p.tm_sg = L->tm_sc_g;
+  p.tm_su = L->tm_sc_u;
+  p.tm_sd = L->tm_sc_d;
   const uint8_t *xs = at<uint8_t>(ws, W.x_split);
   p.h = split_rows(at<uint8_t>(ws, W.h), P, c.d_ff);
   p.hs = at<uint8_t>(ws, W.h_scale);
-  bool ok = encode_scale_blocks(&p.tm_sg, L->sc_gate, wblocks, 1) &&
-            encode_scale_blocks(&p.tm_su, L->sc_up, wblocks, 1) &&
-            encode_scale_blocks(&p.tm_sd, L->sc_down, wblocks, 1) &&
-            encode_scale_blocks(&p.tm_xs, at<uint8_t>(ws, W.x_scale),
+  bool ok = encode_scale_blocks(&p.tm_xs, at<uint8_t>(ws, W.x_scale),
                                 tiles * kBlocks * (c.d_model / 128), kBlocks) &&
             encode_scale_blocks(&p.tm_hs, p.hs, tiles * kBlocks * (c.d_ff / 128), kBlocks);
   for (int i = 0; i < 3; ++i)

@@ -1718,6 +1718,22 @@ moe_status forward_mxfp4(const moe_layer *L, const void *x, int T, void *out, vo
                 c.d_model, static_cast<__nv_bfloat16 *>(out));
 }
 
+// Launch of a conversion kernel: 256 threads, at most `waves` blocks an SM of the current device.  An
+// SM holds 5 to 8 of them at a time; many more, each short, keep the copy engines of every SM busy to
+// the end (185,000 x 4096 bf16: quantisation 352 us with 8 an SM, 328 with 64, 334 with 256; its
+// inverse 354, 307, 291).
+template <typename... KArgs, typename... Args>
+moe_status launch_conversion(void (*kern)(KArgs...), size_t pieces, int unroll, int waves,
+                             void *stream, Args... args) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  const size_t b = (pieces + 256 * unroll - 1) / (256 * unroll), most = (size_t)sms * waves;
+  return launch(kern, dim3((unsigned)(b < most ? b : most)), dim3(256), 0,
+                static_cast<cudaStream_t>(stream), args...);
+}
+
 int mxfp4_launches(const moe_layer *L, int T) {
   if (T == 0) return 0;
   if (few_shape(L->cfg, T)) return 1;
@@ -1891,25 +1907,16 @@ static bool mxfp4_args(const void *m, moe_dtype dtype, long long rows, int cols,
   return aligned16(m) && aligned16(codes);
 }
 
-// 256 threads; at most `waves` blocks an SM.  The device holds 5 to 8 of them at a time; many more,
-// each short, keep the copy engines of every SM busy to the end (185,000 x 4096 bf16: quantisation
-// 352 us with 8 a SM, 328 with 64, 334 with 256; its inverse 354, 307, 291).
-static dim3 mxfp4_grid(size_t pieces, int unroll, int waves) {
-  const size_t b = (pieces + 256 * unroll - 1) / (256 * unroll), most = (size_t)148 * waves;
-  return dim3((unsigned)(b < most ? b : most));
-}
-
 moe_status moe_mxfp4_quantize(const void *src, moe_dtype dtype, long long rows, int cols,
                               uint8_t *codes, uint8_t *scales, void *stream) {
   moe_status s;
   if (!mxfp4_args(src, dtype, rows, cols, codes, scales, &s)) return s;
   const size_t lanes = (size_t)rows * cols / kMxPerLane;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == MOE_BF16)
-    return launch(mxfp4_quantize_kernel<__nv_bfloat16>, mxfp4_grid(lanes, kMxUnroll, 64), dim3(256), 0, st,
-                  static_cast<const __nv_bfloat16 *>(src), lanes, codes, scales);
-  return launch(mxfp4_quantize_kernel<float>, mxfp4_grid(lanes, kMxUnroll, 64), dim3(256), 0, st,
-                static_cast<const float *>(src), lanes, codes, scales);
+    return launch_conversion(mxfp4_quantize_kernel<__nv_bfloat16>, lanes, kMxUnroll, 64, stream,
+                             static_cast<const __nv_bfloat16 *>(src), lanes, codes, scales);
+  return launch_conversion(mxfp4_quantize_kernel<float>, lanes, kMxUnroll, 64, stream,
+                           static_cast<const float *>(src), lanes, codes, scales);
 }
 
 moe_status moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, long long rows,
@@ -1917,12 +1924,11 @@ moe_status moe_mxfp4_dequantize(const uint8_t *codes, const uint8_t *scales, lon
   moe_status s;
   if (!mxfp4_args(dst, dtype, rows, cols, codes, scales, &s)) return s;
   const size_t lanes = (size_t)rows * cols / kMxPerLane;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == MOE_BF16)
-    return launch(mxfp4_dequantize_kernel<__nv_bfloat16>, mxfp4_grid(lanes, kMxUnroll, 256), dim3(256), 0, st,
-                  codes, scales, lanes, static_cast<__nv_bfloat16 *>(dst));
-  return launch(mxfp4_dequantize_kernel<float>, mxfp4_grid(lanes, kMxUnroll, 256), dim3(256), 0, st, codes,
-                scales, lanes, static_cast<float *>(dst));
+    return launch_conversion(mxfp4_dequantize_kernel<__nv_bfloat16>, lanes, kMxUnroll, 256, stream,
+                             codes, scales, lanes, static_cast<__nv_bfloat16 *>(dst));
+  return launch_conversion(mxfp4_dequantize_kernel<float>, lanes, kMxUnroll, 256, stream, codes,
+                           scales, lanes, static_cast<float *>(dst));
 }
 
 moe_status moe_mxfp4_tile_scales(const uint8_t *scales, long long rows, int cols, uint8_t *tiled,
@@ -1932,9 +1938,9 @@ moe_status moe_mxfp4_tile_scales(const uint8_t *scales, long long rows, int cols
   if (!scales || !tiled || rows > (1ll << 62) / cols) return MOE_ERR_INVALID_ARG;
   if (!aligned16(scales) || !aligned16(tiled)) return MOE_ERR_ALIGNMENT;
   const size_t words = (size_t)rows * (cols / 128);
-  return launch(mxfp4_tile_scales_kernel, mxfp4_grid(words, 1, 8), dim3(256), 0,
-                static_cast<cudaStream_t>(stream), reinterpret_cast<const uint32_t *>(scales), words,
-                cols / 128, reinterpret_cast<uint32_t *>(tiled));
+  return launch_conversion(mxfp4_tile_scales_kernel, words, 1, 8, stream,
+                           reinterpret_cast<const uint32_t *>(scales), words, cols / 128,
+                           reinterpret_cast<uint32_t *>(tiled));
 }
 
 moe_status moe_forward_profiled(moe_handle h, const void *x, int n_tokens, void *out,

@@ -3,7 +3,7 @@ dense FFN (d_ff 11264), against the 64-bit form of a sample of tokens (tests/mxf
 import pytest
 import torch
 
-from sparse_moe_layer_warp_b200 import MoELayerMXFP4
+from sparse_moe_layer_warp_b200 import MoELayer, MoELayerMXFP4, mxfp4_dequantize
 from tests import mxfp4_reference as ref
 
 pytestmark = [pytest.mark.gpu, pytest.mark.slow]
@@ -68,3 +68,73 @@ def test_prefill_beside_another_call(cuda_ok, priority):
     torch.cuda.synchronize()
     assert a.layer.device_status() == 0 and b.layer.device_status() == 0
     assert all(torch.equal(o, want_a) for o in oa) and all(torch.equal(o, want_b) for o in ob)
+
+
+def _sample(idx, E):
+    """Tokens that between them meet every expert that any token meets: the first and the last of each,
+    and the batch's ends."""
+    T = idx.shape[0]
+    tok = torch.arange(T, device=idx.device).unsqueeze(1).expand_as(idx).reshape(-1)
+    flat = idx.reshape(-1).long()
+    first = torch.full((E,), T, device=idx.device).scatter_reduce_(0, flat, tok, "amin")
+    last = torch.full((E,), -1, device=idx.device).scatter_reduce_(0, flat, tok, "amax")
+    met = last >= 0
+    ends = torch.tensor([0, T - 1], device=idx.device)
+    return torch.unique(torch.cat((first[met], last[met], ends)))
+
+
+def _check(c, out, layer, weights, mx):
+    idx = layer.route(x=c.x)["idx"]
+    rows = _sample(idx, c.E)
+    assert set(idx[rows].flatten().tolist()) == set(idx.flatten().tolist())
+    want, bound = ref.layer(c.x[rows], c.router, c.bias, *weights, c.k, c.shared, 1.0, mx)
+    over = (out[rows].double() - want).abs() / bound
+    assert not over.isnan().any() and over.max() <= 1, float(over.max())
+
+
+CASES = [
+    dict(T=1, **FULL), dict(T=16, **FULL), dict(T=64, **FULL),  # one launch
+    dict(T=65, **FULL), dict(T=256, **FULL),                    # CTA pairs, 32 rows
+    dict(T=256, **dict(FULL, shared=0)),
+    dict(T=4096, skew=True, **FULL), dict(T=8192, **FULL),      # 112 rows
+    dict(T=8192, **dict(FULL, shared=0)),
+    dict(T=1000, d=4096, E=1, k=1, f=11264, shared=0),          # the dense FFN
+    dict(T=20, d=4096, E=1, k=1, f=11264, shared=0),
+]
+
+
+@pytest.mark.parametrize("kw", CASES, ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items()))
+def test_full_size(cuda_ok, kw):
+    c = Full(**kw)
+    out = c.layer.forward(c.x)
+    weights = [(lambda g, p=p: ref.values(p[0][g], p[1][g])) for p in c.w]
+    _check(c, out, c.layer, weights, True)
+    assert torch.equal(out, c.layer.forward(c.x))
+    assert c.layer.device_status() == 0
+
+
+@pytest.mark.parametrize("kw", CASES[:3], ids=lambda kw: f"T{kw['T']}")
+def test_one_launch_full_size_bf16(cuda_ok, kw):
+    c = Full(**kw)
+    w = [mxfp4_dequantize(*p) for p in c.w]
+    layer = MoELayer(c.router, c.bias, *w, top_k=c.k, max_tokens=kw["T"], n_shared=c.shared)
+    out = layer.forward_few(c.x)
+    _check(c, out, layer, [(lambda g, p=p: p[g].double()) for p in w], False)
+    assert torch.equal(out, layer.forward_few(c.x))
+    assert layer.device_status() == 0
+
+
+# CTA pairs with 32 rows a tile (at most 12 rows an expert on average), with no shared expert
+SMALL = [dict(T=70, d=256, E=64, k=4, f=128, shared=0), dict(T=129, d=640, E=288, k=8, f=384, shared=0),
+         dict(T=200, d=384, E=40, k=2, f=256, shared=0, skew=True)]
+
+
+@pytest.mark.parametrize("kw", SMALL, ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items()))
+def test_small_token_tiles_without_a_shared_expert(cuda_ok, kw):
+    c = Full(**kw)
+    out = c.layer.forward(c.x)
+    weights = [(lambda g, p=p: ref.values(p[0][g], p[1][g])) for p in c.w]
+    want, bound = ref.layer(c.x, c.router, c.bias, *weights, c.k, c.shared, 1.0, True)
+    over = (out.double() - want).abs() / bound
+    assert not over.isnan().any() and over.max() <= 1, float(over.max())
+    assert torch.equal(out, c.layer.forward(c.x)) and c.layer.device_status() == 0

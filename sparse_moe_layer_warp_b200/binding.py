@@ -620,11 +620,25 @@ class MoELayer:
         self._ws_clear = {"ws": False, "bw_ws": False}  # cleared by a call that was not captured
         self._ws_captured = {"ws": False, "bw_ws": False}  # used by a captured call
         self._kept = []  # replaced workspaces that graphs use
+        self._streams = set()  # (raw) streams that read self.tensors
         self.E, self.k, self.d = (int(self.cfg.n_experts), int(self.cfg.top_k),
                                   int(self.cfg.d_model))
 
     def _on(self, stream, *tensors):
         return _on(self.device.index, stream, *tensors)
+
+    def _read(self):
+        """A call on the current stream reads self.tensors: a layer dropped before the call is done (it
+        may hold the last reference to them) gives them back only afterwards."""
+        raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+        if raw not in self._streams:
+            self._streams.add(raw)
+            here = torch.cuda.current_stream()
+            for t in self.tensors:
+                for part in t if isinstance(t, tuple) else (t,):
+                    if part is not None:
+                        part.record_stream(here)
+        return raw
 
     def _expect(self, t, shape, dtype, name):
         _expect(t, shape, dtype, name)
@@ -647,6 +661,7 @@ class MoELayer:
             if logits_out is None:
                 logits_out = on.new(torch.empty((T, self.E), dtype=torch.float32,
                                                 device=self.device))
+            self._read()
             moe_router_logits_static(self.handle, x, T, logits_out, d_model=self.d,
                                      n_experts=self.E, dtype=self.dtype)
         return logits_out
@@ -673,8 +688,7 @@ class MoELayer:
     def _reserve(self, name, need):
         """self.ws or self.bw_ws for a call on the current stream, replaced if it is smaller than need
         bytes."""
-        ws, users = getattr(self, name), self._ws_streams[name]
-        raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+        ws, users, raw = getattr(self, name), self._ws_streams[name], self._read()
         capturing = torch.cuda.is_current_stream_capturing()
         if ws is None or ws.numel() < need:
             # The old one goes back to the pool of the stream that allocated it, once every stream

@@ -210,3 +210,24 @@ def test_first_call_of_a_layer_captured(cuda_ok, mx, T):
         assert torch.equal(out, want)
     assert torch.equal(layer.forward(c.x), want)
     assert layer.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [10, 200])
+def test_layer_dropped_while_a_call_runs(other, T):  # noqa: F811
+    """A converted layer holds the only references to its codes and scales: dropped while a call on another
+    stream is still to run, it gives them (and the workspace) back only after that call."""
+    c = Case(T=T, **KW)
+    trained = c.layer(False)
+    want = trained.to_mxfp4().forward(c.x).clone()
+    served = trained.to_mxfp4()
+    shapes = [t.shape for w in served.tensors[2:] for t in w]
+    out = torch.empty_like(c.x)
+    torch.cuda.synchronize()
+    _hold(other)
+    served.forward(c.x, out=out, stream=other)
+    del served
+    fresh = [torch.empty(s, dtype=torch.uint8, device="cuda").fill_(255) for s in shapes
+             for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert all((t == 255).all() for t in fresh)

@@ -138,3 +138,20 @@ def test_small_token_tiles_without_a_shared_expert(cuda_ok, kw):
     over = (out.double() - want).abs() / bound
     assert not over.isnan().any() and over.max() <= 1, float(over.max())
     assert torch.equal(out, c.layer.forward(c.x)) and c.layer.device_status() == 0
+
+
+def test_one_launch_beside_prefill(cuda_ok):
+    """A cooperative launch of the whole device on one stream, prefill's persistent grids on another."""
+    a, b = Full(8192, **FULL, seed=1), Full(16, **FULL, seed=2)
+    want_a, want_b = a.layer.forward(a.x).clone(), b.layer.forward(b.x).clone()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream(priority=-1)
+    n = 4
+    oa, ob = [torch.empty_like(a.x) for _ in range(n)], [torch.empty_like(b.x) for _ in range(8 * n)]
+    torch.cuda.synchronize()
+    for i in range(n):
+        a.layer.forward(a.x, out=oa[i], stream=sa)
+        for j in range(8):
+            b.layer.forward(b.x, out=ob[8 * i + j], stream=sb)
+    torch.cuda.synchronize()
+    assert a.layer.device_status() == 0 and b.layer.device_status() == 0
+    assert all(torch.equal(o, want_a) for o in oa) and all(torch.equal(o, want_b) for o in ob)

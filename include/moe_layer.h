@@ -235,6 +235,13 @@ moe_status moe_forward(moe_handle h, const void *x, int n_tokens, void *out, voi
  * bit; sums run in another fixed order (deterministic).  bf16 weights: h is rounded to bf16 as in
  * moe_forward; MXFP4: as above.  moe_forward of an MXFP4 handle is this call where it is
  * supported.
+ * When to call it (bf16): it is faster than moe_forward for up to 8 tokens, and beyond that while
+ * there are no more (token, slot) pairs than experts.  (Its token tiles have 8 rows, past 8 tokens
+ * 16, and each passes over its expert's weights; moe_forward's grow with the batch.)  Against
+ * moe_forward, d_model 4096, L2 flushed, us: 288 experts, top-8, d_ff 1280: 73 / 86 at 1 token, 306 / 325 at 8, 519 / 542 at
+ * 16, 833 / 845 at 32, 1058 / 1042 at 48, 1234 / 1187 at 64; 32 experts: 73 / 83, 177 / 178,
+ * 218 / 198, 284 / 208, 357 / 220, 464 / 231; 8 experts, top-2, d_ff 14336: 134 / 182, 454 / 474,
+ * 519 / 477, 664 / 485; one expert of d_ff 11264: 81 / 114, 90 / 116, 158 / 117, 242 / 123.
  * At most 64 tokens, n_tokens * top_k <= 512, n_experts <= 288, d_model <= 8192; otherwise, and
  * for fp32 layers and expert-parallel slices, MOE_ERR_UNSUPPORTED.  A cooperative launch with one
  * block on each SM: it starts when the whole device is free of blocks that hold their SMs'

@@ -721,7 +721,8 @@ class MoELayer:
         return out
 
     def forward_few(self, x, out=None, stream=None):
-        """forward for a few tokens in one launch (bf16; limits in include/moe_layer.h)."""
+        """forward for at most 64 tokens in one launch (bf16 or MXFP4 weights; limits, and from which
+        batch on a bf16 layer's forward is faster, in include/moe_layer.h)."""
         T = self._rows(x)
         if out is not None:
             self._expect(out, x.shape, x.dtype, "out")
@@ -882,9 +883,13 @@ class MoELayer:
 
 class MoELayerMXFP4(MoELayer):
     """MoELayer over MXFP4 expert weights, for serving: w_gate, w_up [E + n_shared, f, d] and
-    w_down [E + n_shared, d, f] are (codes, scales) as mxfp4_quantize returns them (the layer keeps
-    the codes and a tiled copy of the scales); the router and the activations are bf16.  forward, forward_few, route and router_stats as in MoELayer;
-    training calls and expert_health are refused by the library (MoEError)."""
+    w_down [E + n_shared, d, f] are (codes, scales) as mxfp4_quantize returns them; the router and
+    the activations are bf16.  forward, forward_few, route and router_stats as in MoELayer; training
+    calls and expert_health are refused by the library (MoEError).
+
+    The layer reads the caller's codes in place, but a copy of the scales, tiled once when it is
+    made.  Weights written anew into the same tensors would change the one and not the other: other
+    weights need another layer.  Codes start on a 32-byte boundary."""
 
     def __init__(self, w_router, router_bias, w_gate, w_up, w_down, top_k: int,
                  max_tokens: int, n_shared: int = 1, routed_scale: float = 1.0):

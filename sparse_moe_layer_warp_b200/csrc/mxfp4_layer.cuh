@@ -18,7 +18,7 @@
 // Scales are copied to TMEM by tcgen05.cp in the order of the instruction's scale layout: blocks of
 // 512 bytes for 128 rows x 128 K, byte (r % 32) * 16 + r / 32 * 4 + k / 32.
 //
-// Bound at 16 tokens by the weight stream: 884 MB in 171 us, 0.79 of the copy rate (a stage of 17 KB
+// Bound at 16 tokens by the weight stream: 884 MB in 168 to 172 us, 0.79 of the copy rate (a stage of 17 KB
 // of codes fills 33 KB of shared memory, so a ring of 5 or 6 stages holds 90 to 100 KB in flight;
 // asking tiles into L2 ahead of their load made it 14 % slower).  At 1 token (37 us) by latency: 10 us
 // of routing, 14 for up units of 32 stages, 6 for down units of 10, 3 for the combine.

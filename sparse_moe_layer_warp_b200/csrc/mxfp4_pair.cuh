@@ -7,13 +7,14 @@
 // 112 columns of N).  A pair runs M = 256, N = 224: a CTA's codes are read once for 112 tokens, and
 // each CTA holds and reads only half of the token rows -- the hi rows in the leader, the lo rows in
 // its peer.  A stage of 896 clocks then moves 106 KB, and the tensor cores bind (8192 tokens: 1.84
-// ms, the tensor pipe 71 % active, 1.35 GHz under the power cap).  256 tokens stream 2.4 GB of weights
-// in 0.39 ms, 0.94 of the copy rate.
+// to 1.88 ms alone, the tensor pipe 71 % active).  256 tokens stream 2.4 GB of weights in 0.39 to 0.40
+// ms, 0.92 to 0.94 of the copy rate.
 //
 // CTA r of a pair holds weight rows [128 r, 128 r + 128) of each 256-row tile; a unit has two tiles
 // (gate and up; two neighbours of W_d).  N follows the unit's tokens (2 x the next multiple of 8).
-// TMEM: 2 x 224 accumulator columns (of 112-token tiles), so one unit at a time, and two sets of scales.  The scales of
-// all N columns are needed by both CTAs, those of the weight rows by the CTA that holds them.
+// TMEM: 2 x 224 accumulator columns (of 112-token tiles), so one unit at a time, and two sets of
+// scales.  The scales of all N columns are needed by both CTAs, those of the weight rows by the CTA
+// that holds them.
 // The combine is a launch of its own: at these sizes y is larger than L2 and wants every warp.
 #pragma once
 #include <limits.h>
@@ -24,8 +25,8 @@ namespace moe {
 
 constexpr int kMxPairEpiWarps = 16;  // warps 0-15: four for each TMEM lane quadrant
 // then MMA (two warps in the leader: one for each weight tile, as in mxfp4_layer.cuh; the first is the
-// peer's scheduler), weights, token rows.  20 warps: a 21st would leave 80 registers a thread, and
-// the epilogue spilled.
+// peer's scheduler), weights, token rows.  20 warps leave 96 registers a thread: the epilogue of
+// 112-token tiles spills 40 bytes (none with 32).  A 21st warp would leave 80 and spill 116.
 constexpr int kMxPairThreads = 32 * (kMxPairEpiWarps + 4);
 
 struct MxPairParams {
@@ -44,8 +45,8 @@ __host__ __device__ constexpr int pair_box(int i) {
   return i == 2 ? BN : (i == 1 ? BN / 2 : (BN > 32 ? 16 : 8));
 }
 
-// BN: token rows of a tile.  112 where the tensor cores bind.  16 where weights are streamed for a few
-// rows of each expert: what counts is then the ring, six stages against four.
+// BN: token rows of a tile.  112 where the tensor cores bind.  32 where weights are streamed for a few
+// rows of each expert: what counts is then the ring, five stages against four.
 template <int kBN>
 struct MxPairCfg {
   static constexpr int BN = kBN;
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kMxPairThreads, 1)
   uint8_t *sA = smem;                       // [S][2 tiles][128 rows][128 B]
   uint8_t *sB = sA + S * C::A_BYTES;        // [S][BN rows][128 B]
   uint8_t *sSA = sB + S * C::B_BYTES;       // [S][2][512]
-  uint8_t *sSB = sSA + S * C::SA_BYTES;     // [S][1024]
+  uint8_t *sSB = sSA + S * C::SA_BYTES;     // [S][1024] (32 rows: 512)
   uint64_t *full = reinterpret_cast<uint64_t *>(sSB + S * C::SB_BYTES);  // the leader's: both CTAs'
   uint64_t *empty = full + S;
   uint64_t *tfull = empty + S;

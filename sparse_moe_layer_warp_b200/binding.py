@@ -673,10 +673,10 @@ class MoELayer:
         """The workspace, large enough for calls of up to n_tokens tokens and ready for a call on any
         stream."""
         with self._on(stream):
-            before = self.ws
+            before, clear = self.ws, self._ws_clear["ws"]
             ws = self._workspace(n_tokens)
-            if ws is not before and not torch.cuda.is_current_stream_capturing():
-                torch.cuda.current_stream().synchronize()
+            if (ws is not before or not clear) and not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()  # it was cleared just now
         return ws
 
     def _workspace(self, n_tokens: int):

@@ -231,3 +231,26 @@ def test_layer_dropped_while_a_call_runs(other, T):  # noqa: F811
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     assert all((t == 255).all() for t in fresh)
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_workspace_of_a_captured_call_reserved_for_another_stream(other, mx):  # noqa: F811
+    """workspace(T) on the caller's stream, held back, after a layer's first call was captured; then the
+    first call outside the graph on another stream."""
+    c = Case(T=70, **KW)
+    want = c.layer(mx).forward(c.x).clone()
+    layer, out = c.layer(mx), torch.empty_like(c.x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        layer.forward(c.x, out=out)
+    got = torch.empty_like(c.x)
+    layer.ws.fill_(0xAB)
+    _hold()
+    layer.workspace(70)
+    layer.forward(c.x, out=got, stream=other)
+    torch.cuda.synchronize()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(out, want)
+    assert layer.device_status() == 0

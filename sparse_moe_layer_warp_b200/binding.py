@@ -519,7 +519,8 @@ def moe_gemm_clock(handle, ws, stream=None) -> tuple:
 def mxfp4_quantize(w, stream=None):
     """(codes [.., cols / 2], scales [.., cols / 32]), uint8, of `w` [.., cols] (fp32 or bf16,
     contiguous, cols a multiple of 32): MXFP4, one power-of-two scale for 32 neighbours.  On `stream`
-    (default: the current one), which the caller orders after whatever wrote w."""
+    (default: the current one), which the caller orders after whatever wrote w, and which outlives the
+    tensors if it was made elsewhere (ExternalStream): they are recorded on it."""
     dtype = _DTYPE_CODE.get(w.dtype)
     if dtype is None:
         raise ValueError(f"w: expected fp32 or bf16, got {w.dtype}")
@@ -538,7 +539,8 @@ def mxfp4_quantize(w, stream=None):
 
 
 def mxfp4_dequantize(codes, scales, dtype=torch.bfloat16, stream=None):
-    """The values [.., cols] that codes [.., cols / 2] and scales [.., cols / 32] stand for."""
+    """The values [.., cols] that codes [.., cols / 2] and scales [.., cols / 32] stand for, on `stream`
+    as mxfp4_quantize."""
     if dtype not in _DTYPE_CODE:
         raise ValueError(f"dtype: expected fp32 or bf16, got {dtype}")
     *lead, half = codes.shape or (1,)
@@ -583,7 +585,8 @@ class MoELayer:
 
     Calls run on `stream` (None: the current one), which the caller orders after whatever wrote
     their inputs; results, and a workspace that a call has to allocate, come from that stream's
-    pool.  Calls of a layer share its workspace: on several streams the caller orders them.  A
+    pool.  A stream made elsewhere (ExternalStream) outlives the tensors of its calls, which are
+    recorded on it.  Calls of a layer share its workspace: on several streams the caller orders them.  A
     workspace that a captured call uses lives as long as the layer, so its graph may be replayed
     after calls of any size; the graph needs the layer to live."""
 
